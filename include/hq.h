@@ -308,6 +308,115 @@ hq_status hq_hessian_pack_bf16tril(const float* H, int64_t K, uint8_t* out, hq_s
 hq_status hq_hessian_unpack_bf16tril(const uint8_t* in, int64_t K, float* H_full,
                                      hq_stream_t stream);
 
+/*
+ * Weights and activations in 8-bit floating point (e4m3: 1 sign, 4 exponent, 3 mantissa bits,
+ * largest finite value 448), the format a layer is weighed against int4 in, and the product that
+ * runs such a layer.  A scale covers 128 columns of one row (activations) or 128 x 128 entries
+ * (weights); blocks at the right and lower edge are cut by the matrix.  For a block with absolute
+ * maximum a:
+ *     s = fp32(a / 448), r = fp32(448 / a), code = e4m3(fp32(x r)) (ties to even, saturating),
+ *     dequantised value = code * s;
+ *   a == 0: s = 0, codes 0;  0 < a < 2^-100: as if a were 2^-100;  a block holding a NaN or an
+ *   infinity gets a non-finite scale, and its dequantised values are NaN or infinite.
+ * Layouts:
+ *   codes  : uint8, one row of hq_fp8_pitch(K) bytes (K rounded up to 16) for each row of the
+ *            matrix; the quantisers write zeros past column K, the products never read them.
+ *            16-byte aligned.
+ *   scales : fp32, [ceil(K / 128), M] for the M rows of an activation (a block's scales of
+ *            consecutive rows lie together), [ceil(N / 128), ceil(K / 128)] for a weight [N, K].
+ *
+ * hq_fp8_quantize_rows: X [M, K] (x_dtype) -> codes [M, pitch], scales [ceil(K / 128), M].
+ *   M >= 0 (M == 0 is a no-op).
+ * hq_fp8_quantize_blocks: E weights W [E, N, K] (w_dtype) -> codes [E, N, pitch], scales
+ *   [E, ceil(N / 128), ceil(K / 128)].  E >= 1 (1 for one layer, the number of experts otherwise).
+ * K >= 1, N >= 1; K <= 2^24, E * N < 2^31 (N <= 2^22), E <= HQ_MAX_EXPERTS, M <= 2^30
+ * (HQ_ERR_UNSUPPORTED).  Any alignment of X and W that their type allows; 16-byte aligned rows take
+ * 16-byte loads, others element loads with the same results.  Asynchronous; identical run to run.
+ */
+#define HQ_MAX_EXPERTS 1024
+int64_t hq_fp8_pitch(int64_t K); /* 0 for K < 1 */
+hq_status hq_fp8_quantize_rows(const void* X, int x_dtype, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                               hq_stream_t stream);
+hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t N, int64_t K, uint8_t* codes,
+                                 float* scales, hq_stream_t stream);
+
+/*
+ * The product of e4m3 activations and weights:
+ *   Y[m, n] = sum_b sa[b, m] sw[n / 128, b] sum_{k in block b} A[m, k] W[n, k],
+ * the inner sums on the tensor cores, scaled and added over the blocks in fp32, rounded once to
+ * y_dtype (HQ_BF16 or HQ_F32).  Y [rows, N], row-major.
+ * hq_fp8_gemm: one weight for all M rows.  M >= 0 (M == 0 is a no-op).
+ * hq_fp8_linear: the same from activations X [M, K] in x_dtype, quantised into the workspace on the
+ *   way: hq_fp8_quantize_rows followed by hq_fp8_gemm, with the same result.  workspace: device,
+ *   256-byte aligned, at least hq_fp8_linear_workspace_bytes(M, K) bytes (HQ_ERR_WORKSPACE), not
+ *   shared with a call that may run at the same time (another stream, or another captured graph);
+ *   NULL is accepted where that size is 0.
+ * hq_fp8_expert_gemm: rows offsets[e] .. offsets[e + 1] - 1 of A and Y meet weight e of W
+ *   [E, N, K], for every expert.  offsets: DEVICE int32 [E + 1], not decreasing, between 0 and
+ *   `rows` (a range outside is cut to it, an inverted one is empty).  Rows of Y outside every range
+ *   are left as they were; an expert without rows costs nothing.
+ * A NaN or infinity in a row of A reaches that row of Y only, one in W's block the columns of its
+ * 128 rows.  A row's result does not depend on the other rows' values, and is identical run to run.
+ *   dev_status : optional device int; if non-NULL a kernel that hits a bounded-wait timeout stores
+ *            HQ_ERR_TIMEOUT there (the caller zeroes it beforehand).
+ * Asynchronous.  Y must not alias the operands.  Sizes as for the quantisers.  There is no gradient
+ * here: the codes are whole numbers of a layer that has been trained.
+ */
+hq_status hq_fp8_gemm(const uint8_t* a_codes, const float* a_scales, int64_t M, const uint8_t* w_codes,
+                      const float* w_scales, int64_t N, int64_t K, void* Y, int y_dtype, int* dev_status,
+                      hq_stream_t stream);
+size_t hq_fp8_linear_workspace_bytes(int64_t M, int64_t K); /* 0 if the shape is invalid, or M == 0 */
+hq_status hq_fp8_linear(const void* X, int x_dtype, int64_t M, const uint8_t* w_codes, const float* w_scales, int64_t N,
+                        int64_t K, void* Y, int y_dtype, void* workspace, size_t workspace_bytes, int* dev_status,
+                        hq_stream_t stream);
+hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
+                             const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K, void* Y,
+                             int y_dtype, int* dev_status, hq_stream_t stream);
+
+/*
+ * Tokens laid out by expert and back.  A layer of experts sends each of its T tokens to `top` of E
+ * experts; calibration sums one Hessian for each expert from its own tokens (hq_hessian_accumulate
+ * on each range of rows), and the quantised product runs on such ranges (hq_fp8_expert_gemm).
+ *
+ * hq_expert_sort: a stable sort of the choices ids [T, top] by expert.
+ *   ids      : int32 [T, top]; an id outside [0, E) is a dropped choice.  A token may name the same
+ *              expert twice.
+ *   offsets  : int32 [E + 1] out: expert e has rows offsets[e] .. offsets[e + 1] - 1; offsets[E] =
+ *              rows in use, at most T * top.
+ *   order    : int32 [T * top] out: the choice t * top + j of each row, ascending inside an expert;
+ *              entries from offsets[E] on are left as they were.
+ *   position : int32 [T, top] out: each choice's row, -1 for a dropped one.
+ *   workspace: device, 256-byte aligned, at least hq_expert_sort_workspace_bytes(T, top, E) bytes.
+ *   T >= 0, top >= 1, 1 <= E <= HQ_MAX_EXPERTS, T * top <= 2^30 (HQ_ERR_UNSUPPORTED).
+ * hq_expert_dispatch: rows[position[t, j]] = X[t]; X [T, K], rows [T * top, K] in one dtype.  Its
+ *   gradient with respect to X is hq_expert_combine of the rows' gradient with weights NULL.
+ * hq_expert_dispatch_fp8: the same quantised on the way as hq_fp8_quantize_rows would the rows:
+ *   codes [T * top, pitch], scales [ceil(K / 128), T * top].
+ * hq_expert_combine: Y[t] = sum_j weights[t, j] rows[position[t, j]] over the choices that were not
+ *   dropped, in the order of j, in fp32, rounded once.  rows [T * top, K] and Y [T, K] in one dtype,
+ *   weights fp32 [T, top] or NULL (all ones).  A token whose choices are all dropped gets zeros.
+ * hq_expert_combine_backward: dY [T, K], the forward's rows, position and weights ->
+ *   d_rows[position[t, j]] = weights[t, j] dY[t] and d_weights[t, j] = <dY[t], rows[position[t, j]]>
+ *   (summed in fp32; 0 for a dropped choice).
+ * position: as hq_expert_sort writes it, every row at most once; an entry outside [0, T * top)
+ *   counts as dropped.  Rows that no choice names are neither read nor written (whatever they or a
+ *   dropped choice's weight hold).  Outputs must not alias inputs.  K >= 1, K <= 2^24.
+ * Device pointers, asynchronous, identical run to run.  Rows made of 16-byte aligned vectors take
+ * 16-byte accesses, others element accesses with the same results (d_weights: up to fp32 rounding).
+ */
+size_t hq_expert_sort_workspace_bytes(int64_t T, int64_t top, int64_t E);
+hq_status hq_expert_sort(const int32_t* ids, int64_t T, int64_t top, int64_t E, int32_t* offsets, int32_t* order,
+                         int32_t* position, void* workspace, size_t workspace_bytes, hq_stream_t stream);
+hq_status hq_expert_dispatch(const void* X, int dtype, int64_t T, int64_t K, const int32_t* position, int64_t top,
+                             void* rows, hq_stream_t stream);
+hq_status hq_expert_dispatch_fp8(const void* X, int x_dtype, int64_t T, int64_t K, const int32_t* position, int64_t top,
+                                 uint8_t* codes, float* scales, hq_stream_t stream);
+hq_status hq_expert_combine(const void* rows, int dtype, int64_t T, int64_t K, const int32_t* position, int64_t top,
+                            const float* weights, void* Y, hq_stream_t stream);
+hq_status hq_expert_combine_backward(const void* dY, const void* rows, int dtype, int64_t T, int64_t K,
+                                     const int32_t* position, int64_t top, const float* weights, void* d_rows,
+                                     float* d_weights, hq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,5 @@
-"""Python binding of libhq.so: GPTQ int4 weight quantisation and the Bf16TrilDiagF32 codec
-on NVIDIA B200 (sm_100a).
+"""Python binding of libhq.so: GPTQ int4 weight quantisation, the Bf16TrilDiagF32 codec, e4m3
+layers with block scales and the expert layout of tokens, on NVIDIA B200 (sm_100a).
 
 Argument marshalling only: every function checks tensor dtypes, shapes and devices, turns
 them into raw pointers and sizes, and calls the C entry point of the same name (declared in
@@ -33,6 +33,9 @@ HQ_F32 = 0
 HQ_BF16 = 1
 # groups N * (K / group) that hq_rtn_quantize_noalloc's fixed scratch holds (hq.h)
 HQ_RTN_NOALLOC_MAX_GROUPS = 1048576
+
+# experts that one call handles (hq.h)
+HQ_MAX_EXPERTS = 1024
 
 _DTYPE = {torch.float32: HQ_F32, torch.bfloat16: HQ_BF16}
 
@@ -79,6 +82,19 @@ _SIGS = {
     "hq_bf16tril_bytes": (_sz, [_i64]),
     "hq_hessian_pack_bf16tril": (_int, [_vp, _i64, _vp, _vp]),
     "hq_hessian_unpack_bf16tril": (_int, [_vp, _i64, _vp, _vp]),
+    "hq_fp8_pitch": (_i64, [_i64]),
+    "hq_fp8_quantize_rows": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp]),
+    "hq_fp8_quantize_blocks": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "hq_fp8_gemm": (_int, [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _vp, _vp]),
+    "hq_fp8_linear_workspace_bytes": (_sz, [_i64, _i64]),
+    "hq_fp8_linear": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _i64, _vp, _int, _vp, _sz, _vp, _vp]),
+    "hq_fp8_expert_gemm": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _vp]),
+    "hq_expert_sort_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "hq_expert_sort": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "hq_expert_dispatch": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "hq_expert_dispatch_fp8": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "hq_expert_combine": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "hq_expert_combine_backward": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
     "hq_debug_factor": (_int, [_vp, _i64, _f, _vp, _vp, _sz, _vp]),
     "hq_debug_gptq_quantize_impl": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _f, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                            _int, _vp]),
@@ -439,6 +455,167 @@ def hq_hessian_unpack_bf16tril(inp, K: int, H_full, stream=None) -> None:
     _check(lib.hq_hessian_unpack_bf16tril(_ptr(inp), K, _ptr(H_full), _stream(stream)), "hq_hessian_unpack_bf16tril")
 
 
+# --------------------------------------------------------------------------- e4m3 layers, experts
+
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _ptrs(*tensors):
+    """The pointers of contiguous tensors (or None) that all live on the current device."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    ptrs = []
+    for t in tensors:
+        ptrs.append(_ptr(t))
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"expected tensors on the current device (cuda:{dev}), got {t.device}")
+    return ptrs
+
+
+def _want(t, name: str, dtype, shape) -> None:
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _pitch(K: int) -> int:
+    return (K + 15) // 16 * 16
+
+
+def hq_fp8_pitch(K: int) -> int:
+    """Bytes of a row of codes."""
+    return int(lib.hq_fp8_pitch(int(K)))
+
+
+def hq_fp8_quantize_rows(X, codes, scales, stream=None) -> None:
+    """X [M, K] -> e4m3 codes [M, pitch] (float8_e4m3fn or uint8) and scales fp32 [ceil(K/128), M]."""
+    M, K = X.shape
+    _want(codes, "codes", _FP8, (M, _pitch(K)))
+    _want(scales, "scales", torch.float32, (_blocks(K), M))
+    x, c, s = _ptrs(X, codes, scales)
+    _check(lib.hq_fp8_quantize_rows(x, _dtype(X), M, K, c, s, _stream(stream)), "hq_fp8_quantize_rows")
+
+
+def hq_fp8_quantize_blocks(W, codes, scales, stream=None) -> None:
+    """W [N, K] or [E, N, K] -> codes [.., N, pitch] and scales fp32 [.., ceil(N/128), ceil(K/128)]."""
+    *lead, N, K = W.shape
+    if len(lead) > 1:
+        raise ValueError("W must be [N, K] or [E, N, K]")
+    _want(codes, "codes", _FP8, (*lead, N, _pitch(K)))
+    _want(scales, "scales", torch.float32, (*lead, _blocks(N), _blocks(K)))
+    w, c, s = _ptrs(W, codes, scales)
+    _check(lib.hq_fp8_quantize_blocks(w, _dtype(W), lead[0] if lead else 1, N, K, c, s, _stream(stream)),
+           "hq_fp8_quantize_blocks")
+
+
+def hq_fp8_gemm(a_codes, a_scales, w_codes, w_scales, K: int, Y, dev_status=None, stream=None) -> None:
+    """Y [M, N] = the product of quantised activations [M, pitch] and a quantised weight [N, pitch]."""
+    M, N = Y.shape
+    _want(a_codes, "a_codes", _FP8, (M, _pitch(K)))
+    _want(a_scales, "a_scales", torch.float32, (_blocks(K), M))
+    _want(w_codes, "w_codes", _FP8, (N, _pitch(K)))
+    _want(w_scales, "w_scales", torch.float32, (_blocks(N), _blocks(K)))
+    a, sa, w, sw, y, st = _ptrs(a_codes, a_scales, w_codes, w_scales, Y, dev_status)
+    _check(lib.hq_fp8_gemm(a, sa, M, w, sw, N, K, y, _dtype(Y), st, _stream(stream)), "hq_fp8_gemm")
+
+
+def hq_fp8_linear_workspace_bytes(M: int, K: int) -> int:
+    return int(lib.hq_fp8_linear_workspace_bytes(int(M), int(K)))
+
+
+def hq_fp8_linear(X, w_codes, w_scales, Y, workspace, dev_status=None, stream=None) -> None:
+    """Y [M, N] = X [M, K], quantised on the way, times a quantised weight [N, pitch]."""
+    M, K = X.shape
+    N = w_codes.shape[0]
+    _want(w_codes, "w_codes", _FP8, (N, _pitch(K)))
+    _want(w_scales, "w_scales", torch.float32, (_blocks(N), _blocks(K)))
+    if tuple(Y.shape) != (M, N):
+        raise ValueError(f"Y must have shape {(M, N)}, not {tuple(Y.shape)}")
+    x, w, sw, y, ws, st = _ptrs(X, w_codes, w_scales, Y, workspace, dev_status)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.hq_fp8_linear(x, _dtype(X), M, w, sw, N, K, y, _dtype(Y), ws, nbytes, st, _stream(stream)),
+           "hq_fp8_linear")
+
+
+def hq_fp8_expert_gemm(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y, dev_status=None, stream=None) -> None:
+    """Rows offsets[e] .. offsets[e + 1] - 1 of Y [rows, N] = those rows of the quantised activations
+    [rows, pitch] times weight e of the quantised [E, N, pitch]; offsets int32 [E + 1], on the device."""
+    rows, N = Y.shape
+    E = w_codes.shape[0]
+    _want(a_codes, "a_codes", _FP8, (rows, _pitch(K)))
+    _want(a_scales, "a_scales", torch.float32, (_blocks(K), rows))
+    _want(offsets, "offsets", torch.int32, (E + 1,))
+    _want(w_codes, "w_codes", _FP8, (E, N, _pitch(K)))
+    _want(w_scales, "w_scales", torch.float32, (E, _blocks(N), _blocks(K)))
+    a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
+    _check(lib.hq_fp8_expert_gemm(a, sa, rows, off, w, sw, E, N, K, y, _dtype(Y), st, _stream(stream)),
+           "hq_fp8_expert_gemm")
+
+
+def hq_expert_sort_workspace_bytes(T: int, top: int, E: int) -> int:
+    return int(lib.hq_expert_sort_workspace_bytes(int(T), int(top), int(E)))
+
+
+def hq_expert_sort(ids, E: int, offsets, order, position, workspace, stream=None) -> None:
+    """Stable sort of the choices ids (int32 [T, top]) by expert: offsets [E + 1], order [T * top]
+    and position [T, top], all int32; -1 in position for an id outside [0, E)."""
+    T, top = ids.shape
+    _want(ids, "ids", torch.int32, (T, top))
+    _want(offsets, "offsets", torch.int32, (E + 1,))
+    _want(order, "order", torch.int32, (T * top,))
+    _want(position, "position", torch.int32, (T, top))
+    i, off, o, p, ws = _ptrs(ids, offsets, order, position, workspace)
+    _check(lib.hq_expert_sort(i, T, top, E, off, o, p, ws, workspace.numel() * workspace.element_size(),
+                              _stream(stream)), "hq_expert_sort")
+
+
+def hq_expert_dispatch(X, position, rows, stream=None) -> None:
+    """rows[position[t, j]] = X[t]; X [T, K], position int32 [T, top], rows [T * top, K]."""
+    (T, K), top = X.shape, position.shape[1]
+    _want(position, "position", torch.int32, (T, top))
+    _want(rows, "rows", X.dtype, (T * top, K))
+    x, p, r = _ptrs(X, position, rows)
+    _check(lib.hq_expert_dispatch(x, _dtype(X), T, K, p, top, r, _stream(stream)), "hq_expert_dispatch")
+
+
+def hq_expert_dispatch_fp8(X, position, codes, scales, stream=None) -> None:
+    """The same with the rows quantised: codes [T * top, pitch], scales fp32 [ceil(K/128), T * top]."""
+    (T, K), top = X.shape, position.shape[1]
+    _want(position, "position", torch.int32, (T, top))
+    _want(codes, "codes", _FP8, (T * top, _pitch(K)))
+    _want(scales, "scales", torch.float32, (_blocks(K), T * top))
+    x, p, c, s = _ptrs(X, position, codes, scales)
+    _check(lib.hq_expert_dispatch_fp8(x, _dtype(X), T, K, p, top, c, s, _stream(stream)), "hq_expert_dispatch_fp8")
+
+
+def hq_expert_combine(rows, position, weights, Y, stream=None) -> None:
+    """Y[t] = sum_j weights[t, j] rows[position[t, j]]; weights fp32 [T, top] or None (all ones)."""
+    (T, K), top = Y.shape, position.shape[1]
+    _want(position, "position", torch.int32, (T, top))
+    _want(rows, "rows", Y.dtype, (T * top, K))
+    if weights is not None:
+        _want(weights, "weights", torch.float32, (T, top))
+    r, p, w, y = _ptrs(rows, position, weights, Y)
+    _check(lib.hq_expert_combine(r, _dtype(Y), T, K, p, top, w, y, _stream(stream)), "hq_expert_combine")
+
+
+def hq_expert_combine_backward(dY, rows, position, weights, d_rows, d_weights, stream=None) -> None:
+    """d_rows[position[t, j]] = weights[t, j] dY[t], d_weights[t, j] = <dY[t], rows[position[t, j]]>."""
+    (T, K), top = dY.shape, position.shape[1]
+    _want(position, "position", torch.int32, (T, top))
+    _want(rows, "rows", dY.dtype, (T * top, K))
+    _want(d_rows, "d_rows", dY.dtype, (T * top, K))
+    _want(weights, "weights", torch.float32, (T, top))
+    _want(d_weights, "d_weights", torch.float32, (T, top))
+    g, r, p, w, dr, dw = _ptrs(dY, rows, position, weights, d_rows, d_weights)
+    _check(lib.hq_expert_combine_backward(g, r, _dtype(dY), T, K, p, top, w, dr, dw, _stream(stream)),
+           "hq_expert_combine_backward")
+
+
 # --------------------------------------------------------------------------- allocation helpers
 
 def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
@@ -450,3 +627,23 @@ def gptq_outputs(N: int, K: int, group: int, device="cuda"):
     codes = torch.empty((N, K // 2), dtype=torch.uint8, device=device)
     scales = torch.empty((N, K // group), dtype=torch.float32, device=device)
     return codes, scales
+
+
+def fp8_rows_outputs(M: int, K: int, device="cuda"):
+    """Codes [M, pitch] and scales [ceil(K/128), M] of quantised activations."""
+    return (torch.empty((M, _pitch(K)), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((_blocks(K), M), dtype=torch.float32, device=device))
+
+
+def fp8_blocks_outputs(N: int, K: int, E: int | None = None, device="cuda"):
+    """Codes [N, pitch] and scales [ceil(N/128), ceil(K/128)] of a quantised weight; [E, ..] with E."""
+    lead = () if E is None else (E,)
+    return (torch.empty((*lead, N, _pitch(K)), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((*lead, _blocks(N), _blocks(K)), dtype=torch.float32, device=device))
+
+
+def expert_sort_outputs(T: int, top: int, E: int, device="cuda"):
+    """offsets [E + 1], order [T * top] and position [T, top]."""
+    return (torch.empty(E + 1, dtype=torch.int32, device=device),
+            torch.empty(T * top, dtype=torch.int32, device=device),
+            torch.empty((T, top), dtype=torch.int32, device=device))

@@ -7,6 +7,7 @@
 #include "../../include/hq.h"
 #include "../../include/hq_debug.h"
 #include "common.cuh"
+#include "fp8_quant.cuh"
 #include "kernels.cuh"
 
 namespace hq {
@@ -57,6 +58,57 @@ hq_status gptq_common(const void* W, int w_dtype, int64_t N, int64_t K, const fl
   st = launch_gptq(W, w_dtype, N, K, H, group, damp, imp, codes, scales, qerr_dev, ws, update_impl, s);
   if (st != HQ_OK) return st;
   return finish_sync(s, reinterpret_cast<const WsHeader*>(ws + L.header), qerr_out);
+}
+
+bool dtype_aligned(const void* p, int dtype) { return aligned(p, dtype == HQ_BF16 ? 2 : 4); }
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;   // rows of an activation, choices of a router
+constexpr int64_t kMaxK = int64_t(1) << 24;
+constexpr int64_t kMaxN = int64_t(1) << 22;
+
+// Sizes of E e4m3 weights [N, K].
+hq_status check_fp8_weight(int64_t E, int64_t N, int64_t K) {
+  if (E < 1 || N < 1 || K < 1) return HQ_ERR_INVALID;
+  if (E > kMaxExperts || N > kMaxN || K > kMaxK || E * N > 0x7FFFFFFF) return HQ_ERR_UNSUPPORTED;
+  return HQ_OK;
+}
+
+hq_status check_fp8_rows(int64_t M, int64_t K) {
+  if (M < 0 || K < 1) return HQ_ERR_INVALID;
+  if (M > kMaxRows || K > kMaxK) return HQ_ERR_UNSUPPORTED;
+  return HQ_OK;
+}
+
+hq_status check_fp8_gemm(const Fp8Gemm& g) {
+  hq_status st = check_fp8_weight(g.E, g.N, g.K);
+  if (st != HQ_OK) return st;
+  st = check_fp8_rows(g.rows, g.K);
+  if (st != HQ_OK) return st;
+  if (!valid_dtype(g.y_dtype)) return HQ_ERR_INVALID;
+  if (g.rows == 0) return HQ_OK;
+  if (g.a_codes == nullptr || g.a_scales == nullptr || g.w_codes == nullptr || g.w_scales == nullptr || g.Y == nullptr)
+    return HQ_ERR_INVALID;
+  if (!aligned(g.a_codes, 16) || !aligned(g.w_codes, 16) || !aligned(g.a_scales, 4) || !aligned(g.w_scales, 4) ||
+      !dtype_aligned(g.Y, g.y_dtype))
+    return HQ_ERR_INVALID;
+  return HQ_OK;
+}
+
+size_t fp8_linear_scales_offset(int64_t M, int64_t K) { return round_up(static_cast<size_t>(M) * fp8_pitch(K), 256); }
+size_t fp8_linear_workspace(int64_t M, int64_t K) {
+  return fp8_linear_scales_offset(M, K) + round_up(static_cast<size_t>(M) * ceil_div(K, 128) * sizeof(float), 256);
+}
+
+// Sizes of a router's choices, and of the rows they name.
+hq_status check_choices(int64_t T, int64_t top) {
+  if (T < 0 || top < 1) return HQ_ERR_INVALID;
+  if (T > kMaxRows || top > kMaxRows || T * top > kMaxRows) return HQ_ERR_UNSUPPORTED;
+  return HQ_OK;
+}
+hq_status check_expert_rows(int dtype, int64_t T, int64_t top, int64_t K) {
+  if (!valid_dtype(dtype)) return HQ_ERR_INVALID;
+  const hq_status st = check_choices(T, top);
+  return st != HQ_OK ? st : check_fp8_rows(0, K);
 }
 
 // qerr = sqrt(num / den) from the two sums, 0 for an all-zero layer (the qerr finaliser's rule).
@@ -434,6 +486,134 @@ hq_status hq_hessian_unpack_bf16tril(const uint8_t* in, int64_t K, float* H_full
   if (!aligned(in, 16) || !aligned(H_full, 4)) return HQ_ERR_INVALID;
   if (K > (int64_t(1) << 20)) return HQ_ERR_UNSUPPORTED;
   return launch_tril_decode(in, K, H_full, static_cast<cudaStream_t>(stream));
+}
+
+int64_t hq_fp8_pitch(int64_t K) { return K < 1 ? 0 : fp8_pitch(K); }
+
+hq_status hq_fp8_quantize_rows(const void* X, int x_dtype, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                               hq_stream_t stream) {
+  if (!valid_dtype(x_dtype)) return HQ_ERR_INVALID;
+  const hq_status st = check_fp8_rows(M, K);
+  if (st != HQ_OK || M == 0) return st;
+  if (X == nullptr || codes == nullptr || scales == nullptr) return HQ_ERR_INVALID;
+  if (!dtype_aligned(X, x_dtype) || !aligned(codes, 16) || !aligned(scales, 4)) return HQ_ERR_INVALID;
+  return launch_fp8_rows(X, x_dtype, M, K, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t N, int64_t K, uint8_t* codes,
+                                 float* scales, hq_stream_t stream) {
+  if (!valid_dtype(w_dtype)) return HQ_ERR_INVALID;
+  const hq_status st = check_fp8_weight(E, N, K);
+  if (st != HQ_OK) return st;
+  if (W == nullptr || codes == nullptr || scales == nullptr) return HQ_ERR_INVALID;
+  if (!dtype_aligned(W, w_dtype) || !aligned(codes, 16) || !aligned(scales, 4)) return HQ_ERR_INVALID;
+  return launch_fp8_blocks(W, w_dtype, E, N, K, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_fp8_gemm(const uint8_t* a_codes, const float* a_scales, int64_t M, const uint8_t* w_codes,
+                      const float* w_scales, int64_t N, int64_t K, void* Y, int y_dtype, int* dev_status,
+                      hq_stream_t stream) {
+  const Fp8Gemm g{a_codes, a_scales, M, nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status};
+  const hq_status st = check_fp8_gemm(g);
+  if (st != HQ_OK || M == 0) return st;
+  return launch_fp8_gemm(g, static_cast<cudaStream_t>(stream));
+}
+
+size_t hq_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
+  return check_fp8_rows(M, K) == HQ_OK ? fp8_linear_workspace(M, K) : 0;
+}
+
+hq_status hq_fp8_linear(const void* X, int x_dtype, int64_t M, const uint8_t* w_codes, const float* w_scales, int64_t N,
+                        int64_t K, void* Y, int y_dtype, void* workspace, size_t workspace_bytes, int* dev_status,
+                        hq_stream_t stream) {
+  if (!valid_dtype(x_dtype)) return HQ_ERR_INVALID;
+  hq_status st = check_fp8_rows(M, K);
+  if (st != HQ_OK) return st;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  const Fp8Gemm g{codes, reinterpret_cast<const float*>(codes + (M > 0 ? fp8_linear_scales_offset(M, K) : 0)), M,
+                  nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status};
+  if (M > 0 && (X == nullptr || !dtype_aligned(X, x_dtype))) return HQ_ERR_INVALID;
+  if (M > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < fp8_linear_workspace(M, K)))
+    return HQ_ERR_WORKSPACE;
+  st = check_fp8_gemm(g);
+  if (st != HQ_OK || M == 0) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = launch_fp8_rows(X, x_dtype, M, K, codes, const_cast<float*>(g.a_scales), s);
+  if (st != HQ_OK) return st;
+  return launch_fp8_gemm(g, s);
+}
+
+hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
+                             const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K, void* Y,
+                             int y_dtype, int* dev_status, hq_stream_t stream) {
+  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status};
+  const hq_status st = check_fp8_gemm(g);
+  if (st != HQ_OK || rows == 0) return st;
+  if (offsets == nullptr || !aligned(offsets, 4)) return HQ_ERR_INVALID;
+  return launch_fp8_gemm(g, static_cast<cudaStream_t>(stream));
+}
+
+size_t hq_expert_sort_workspace_bytes(int64_t T, int64_t top, int64_t E) {
+  if (check_choices(T, top) != HQ_OK || E < 1 || E > kMaxExperts) return 0;
+  return expert_sort_workspace(T * top, E);
+}
+
+hq_status hq_expert_sort(const int32_t* ids, int64_t T, int64_t top, int64_t E, int32_t* offsets, int32_t* order,
+                         int32_t* position, void* workspace, size_t workspace_bytes, hq_stream_t stream) {
+  const hq_status st = check_choices(T, top);
+  if (st != HQ_OK) return st;
+  if (E < 1 || offsets == nullptr || !aligned(offsets, 4)) return HQ_ERR_INVALID;
+  if (E > kMaxExperts) return HQ_ERR_UNSUPPORTED;
+  if (T > 0 && (ids == nullptr || order == nullptr || position == nullptr)) return HQ_ERR_INVALID;
+  if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(position, 4)) return HQ_ERR_INVALID;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < expert_sort_workspace(T * top, E))
+    return HQ_ERR_WORKSPACE;
+  return launch_expert_sort(ids, T * top, E, offsets, order, position, static_cast<uint8_t*>(workspace),
+                            static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_expert_dispatch(const void* X, int dtype, int64_t T, int64_t K, const int32_t* position, int64_t top,
+                             void* rows, hq_stream_t stream) {
+  const hq_status st = check_expert_rows(dtype, T, top, K);
+  if (st != HQ_OK || T == 0) return st;
+  if (X == nullptr || position == nullptr || rows == nullptr) return HQ_ERR_INVALID;
+  if (!dtype_aligned(X, dtype) || !dtype_aligned(rows, dtype) || !aligned(position, 4)) return HQ_ERR_INVALID;
+  return launch_expert_dispatch(X, dtype, T, K, position, top, rows, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_expert_dispatch_fp8(const void* X, int x_dtype, int64_t T, int64_t K, const int32_t* position, int64_t top,
+                                 uint8_t* codes, float* scales, hq_stream_t stream) {
+  const hq_status st = check_expert_rows(x_dtype, T, top, K);
+  if (st != HQ_OK || T == 0) return st;
+  if (X == nullptr || position == nullptr || codes == nullptr || scales == nullptr) return HQ_ERR_INVALID;
+  if (!dtype_aligned(X, x_dtype) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(position, 4))
+    return HQ_ERR_INVALID;
+  return launch_expert_dispatch_fp8(X, x_dtype, T, K, position, top, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_expert_combine(const void* rows, int dtype, int64_t T, int64_t K, const int32_t* position, int64_t top,
+                            const float* weights, void* Y, hq_stream_t stream) {
+  const hq_status st = check_expert_rows(dtype, T, top, K);
+  if (st != HQ_OK || T == 0) return st;
+  if (rows == nullptr || position == nullptr || Y == nullptr) return HQ_ERR_INVALID;
+  if (!dtype_aligned(rows, dtype) || !dtype_aligned(Y, dtype) || !aligned(position, 4) || !aligned(weights, 4))
+    return HQ_ERR_INVALID;
+  return launch_expert_combine(rows, dtype, T, K, position, top, weights, Y, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_expert_combine_backward(const void* dY, const void* rows, int dtype, int64_t T, int64_t K,
+                                     const int32_t* position, int64_t top, const float* weights, void* d_rows,
+                                     float* d_weights, hq_stream_t stream) {
+  const hq_status st = check_expert_rows(dtype, T, top, K);
+  if (st != HQ_OK || T == 0) return st;
+  if (dY == nullptr || rows == nullptr || position == nullptr || weights == nullptr || d_rows == nullptr ||
+      d_weights == nullptr)
+    return HQ_ERR_INVALID;
+  if (!dtype_aligned(dY, dtype) || !dtype_aligned(rows, dtype) || !dtype_aligned(d_rows, dtype) ||
+      !aligned(position, 4) || !aligned(weights, 4) || !aligned(d_weights, 4))
+    return HQ_ERR_INVALID;
+  return launch_expert_combine_backward(dY, rows, dtype, T, K, position, top, weights, d_rows, d_weights,
+                                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,479 @@
+// Tokens laid out by expert and back: a stable counting sort of the router's choices, the copy of
+// each token's row to its places (as it is, or quantised to e4m3 on the way), the weighted sum of
+// the experts' outputs back in token order, and that sum's gradient.
+//
+// A choice is a flat index i = t * top + j into ids [T, top]; position[i] is its row in the sorted
+// layout, or -1 for an id outside [0, E) (a dropped choice: nothing is read, written or counted for
+// it).  Every kernel checks a position against the number of rows before it uses it, so that a
+// wrong one is treated as dropped.
+#include "common.cuh"
+#include "fp8_quant.cuh"
+#include "kernels.cuh"
+
+namespace hq {
+
+// ---------------------------------------------------------------- sort
+//
+// The ids are cut into chunks, one per CTA.  expert_hist_kernel counts each chunk's ids by expert;
+// expert_place_kernel gives every chunk its first row in each expert (the counts of the chunks
+// before it and of the experts before), and ranks the ids inside it.  There each warp owns a
+// contiguous part of the chunk and counts it first, so that its own first rows are known and the
+// ranking runs without any exchange between warps: 32 ids at a time, a lane's rank among the equal
+// ids of its warp comes from a match over the warp.  One chunk (up to kSortOneChunk ids) needs no
+// counts from the others: one launch.  Integer counts only, so the order is the same every time.
+constexpr int kSortWarps = 16;
+constexpr int kSortChunk = 2048;     // ids per CTA of a long list, at least
+constexpr int kSortOneChunk = 8192;  // up to here one CTA sorts alone
+constexpr int kSortMaxCtas = 148;
+
+struct SortSplit {
+  int chunks;
+  int64_t chunk;  // ids per chunk
+};
+static SortSplit sort_split(int64_t R) {
+  if (R <= kSortOneChunk) return {1, R};
+  int64_t chunk = ceil_div(R, kSortMaxCtas);
+  if (chunk < kSortChunk) chunk = kSortChunk;
+  return {static_cast<int>(ceil_div(R, chunk)), chunk};
+}
+
+size_t expert_sort_workspace(int64_t R, int64_t E) {
+  const SortSplit sp = sort_split(R);
+  return sp.chunks == 1 ? 256 : round_up(static_cast<size_t>(sp.chunks) * E * sizeof(int), 256);
+}
+
+__global__ void __launch_bounds__(32 * kSortWarps)
+    expert_hist_kernel(const int* __restrict__ ids, int64_t R, int64_t chunk, int E, int* __restrict__ hist) {
+  extern __shared__ int count[];
+  for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
+  __syncthreads();
+  const int64_t i0 = blockIdx.x * chunk, i1 = min(R, i0 + chunk);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
+    const unsigned e = static_cast<unsigned>(ids[i]);
+    if (e < static_cast<unsigned>(E)) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) hist[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
+}
+
+// Exclusive sum over the CTA's 512 threads of one int each; every thread calls it.
+__device__ __forceinline__ int block_exclusive_sum(int v, int* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  return before + x - v;
+}
+
+// hist == nullptr: one chunk, whose own counts are the totals.
+__global__ void __launch_bounds__(32 * kSortWarps)
+    expert_place_kernel(const int* __restrict__ ids, int64_t R, int64_t chunk, int E, const int* __restrict__ hist,
+                        int* __restrict__ offsets, int* __restrict__ order, int* __restrict__ position) {
+  extern __shared__ int next[];  // [warps][E]: the next row of each expert for each warp's ids
+  __shared__ int warp_sum[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i0 = blockIdx.x * chunk, i1 = min(R, i0 + chunk);
+  const int64_t part = (i1 - i0 + 32 * kSortWarps - 1) / (32 * kSortWarps) * 32;
+  const int64_t w0 = min(i1, i0 + warp * part), w1 = min(i1, w0 + part);
+
+  for (int k = threadIdx.x; k < kSortWarps * E; k += blockDim.x) next[k] = 0;
+  __syncthreads();
+  for (int64_t i = w0 + lane; i < w1; i += 32) {
+    const unsigned e = static_cast<unsigned>(ids[i]);
+    if (e < static_cast<unsigned>(E)) atomicAdd(&next[warp * E + e], 1);
+  }
+  __syncthreads();
+
+  int base = 0;  // rows of the experts handled so far
+  for (int eb = 0; eb < E; eb += blockDim.x) {
+    const int e = eb + threadIdx.x;
+    int total = 0, before = 0;
+    if (e < E) {
+      if (hist != nullptr) {
+        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+          const int c = hist[static_cast<int64_t>(b) * E + e];
+          if (b < static_cast<int>(blockIdx.x)) before += c;
+          total += c;
+        }
+      } else {
+        for (int w = 0; w < kSortWarps; ++w) total += next[w * E + e];
+      }
+    }
+    const int first = base + block_exclusive_sum(total, warp_sum);
+    if (e < E) {
+      int at = first + before;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = next[w * E + e];
+        next[w * E + e] = at;
+        at += c;
+      }
+      if (blockIdx.x == 0) {
+        offsets[e] = first;
+        if (e == E - 1) offsets[E] = first + total;
+      }
+    }
+    // every warp's sums were read before any thread gets here, and are not written again until the
+    // next call's first barrier
+    for (int w = 0; w < kSortWarps; ++w) base += warp_sum[w];
+    __syncthreads();
+  }
+
+  for (int64_t i = w0 + lane; i - lane < w1; i += 32) {
+    const unsigned e = i < w1 ? static_cast<unsigned>(ids[i]) : 0xFFFFFFFFu;
+    const bool kept = e < static_cast<unsigned>(E);
+    const unsigned same = __match_any_sync(0xffffffffu, kept ? e : 0xFFFFFFFFu);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    int at = 0;
+    if (kept) at = next[warp * E + e] + rank;
+    __syncwarp();
+    if (kept && rank == __popc(same) - 1) next[warp * E + e] = at + 1;
+    __syncwarp();
+    if (i < w1 && HQ_IN_BOUNDS(!kept || (at >= 0 && at < R))) {
+      position[i] = kept ? at : -1;
+      if (kept) order[at] = static_cast<int>(i);
+    }
+  }
+}
+
+hq_status launch_expert_sort(const int* ids, int64_t R, int64_t E, int* offsets, int* order, int* position,
+                             uint8_t* ws, cudaStream_t s) {
+  const SortSplit sp = sort_split(R);
+  const int e = static_cast<int>(E);
+  int* hist = nullptr;
+  if (sp.chunks > 1) {
+    hist = reinterpret_cast<int*>(ws);
+    expert_hist_kernel<<<sp.chunks, 32 * kSortWarps, E * sizeof(int), s>>>(ids, R, sp.chunk, e, hist);
+    HQ_LAUNCH_CHECK();
+  }
+  const size_t smem = static_cast<size_t>(kSortWarps) * E * sizeof(int);
+  HQ_CUDA_TRY(cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(kSortWarps * kMaxExperts * sizeof(int))));
+  expert_place_kernel<<<sp.chunks, 32 * kSortWarps, smem, s>>>(ids, R, sp.chunk, e, hist, offsets, order, position);
+  HQ_LAUNCH_CHECK();
+  return HQ_OK;
+}
+
+// ---------------------------------------------------------------- rows in vectors
+//
+// The row kernels below give each token a group of 32 .. 256 threads (as many as its row has
+// vectors, in powers of two), and each thread one vector of 16 bytes at a time; rows that are not
+// made of aligned 16-byte vectors are walked element by element by the same code.
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / sizeof(T);
+  __device__ static void load(const T* p, float (&v)[kN]);
+  __device__ static void store(T* p, const float (&v)[kN]);
+};
+template <>
+__device__ __forceinline__ void Vec<__nv_bfloat16>::load(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void Vec<__nv_bfloat16>::store(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ void Vec<float>::load(const float* p, float (&v)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = a.z;
+  v[3] = a.w;
+}
+template <>
+__device__ __forceinline__ void Vec<float>::store(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename T>
+struct One {  // one element
+  static constexpr int kN = 1;
+  __device__ static void load(const T* p, float (&v)[1]) { v[0] = static_cast<float>(*p); }
+  __device__ static void store(T* p, const float (&v)[1]) { *p = static_cast<T>(v[0]); }
+};
+
+constexpr int kRowThreads = 256;
+// threads per token: enough for one vector each, 32 .. 256
+static int row_threads(int64_t vectors) {
+  int t = 32;
+  while (t < kRowThreads && t < vectors) t *= 2;
+  return t;
+}
+
+// ---------------------------------------------------------------- dispatch
+
+// rows[position[t, j]] = X[t]: a token's row is read once and stored to each of its places.
+template <typename T, template <typename> class V>
+__global__ void __launch_bounds__(kRowThreads)
+    expert_dispatch_kernel(const T* __restrict__ X, int64_t tokens, int64_t K, const int* __restrict__ position, int top,
+                           int64_t rows, int tpt, T* __restrict__ out) {
+  constexpr int N = V<T>::kN;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
+  if (t >= tokens) return;
+  const int64_t vectors = K / N;
+  const int* pos = position + t * top;
+  for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
+    float v[N];
+    V<T>::load(X + t * K + i * N, v);
+    for (int j = 0; j < top; ++j) {
+      const int p = __ldg(pos + j);
+      if (p >= 0 && p < rows) V<T>::store(out + static_cast<int64_t>(p) * K + i * N, v);
+    }
+  }
+}
+
+// The same with the row quantised on the way: once per token, whatever the number of its places.
+// A warp takes 512 columns of one token.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    expert_dispatch_fp8_kernel(const T* __restrict__ X, int64_t tokens, int64_t K, int64_t pitch, bool vec,
+                               const int* __restrict__ position, int top, int64_t rows, uint8_t* __restrict__ codes,
+                               float* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (t >= tokens) return;
+  const int64_t col = static_cast<int64_t>(blockIdx.y) * 512 + lane * 16;
+  float v[16];
+  fp8_load16(X + t * K, col, K, vec, v);
+  float scale;
+  const uint4 c = fp8_quantise_row16(v, scale);
+  const int* pos = position + t * top;
+  for (int j = 0; j < top; ++j) {
+    const int p = __ldg(pos + j);
+    if (p < 0 || p >= rows) continue;
+    if (col < pitch && HQ_IN_BOUNDS(col + 16 <= pitch))
+      *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(p) * pitch + col) = c;
+    if ((lane & 7) == 0 && col < K) scales[(col / kFp8Block) * rows + p] = scale;
+  }
+}
+
+// ---------------------------------------------------------------- combine
+
+// Y[t] = sum_j w[t, j] rows[position[t, j]] in the order of j, summed in fp32 and rounded once.
+template <typename T, template <typename> class V>
+__global__ void __launch_bounds__(kRowThreads)
+    expert_combine_kernel(const T* __restrict__ rows, int64_t nrows, int64_t K, const int* __restrict__ position,
+                          const float* __restrict__ weights, int64_t tokens, int top, int tpt, T* __restrict__ Y) {
+  constexpr int N = V<T>::kN;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
+  if (t >= tokens) return;
+  const int64_t vectors = K / N;
+  const int* pos = position + t * top;
+  for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
+    float acc[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    for (int j = 0; j < top; ++j) {
+      const int p = __ldg(pos + j);
+      if (p < 0 || p >= nrows) continue;
+      const float w = weights != nullptr ? __ldg(weights + t * top + j) : 1.f;
+      float z[N];
+      V<T>::load(rows + static_cast<int64_t>(p) * K + i * N, z);
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] = fmaf(w, z[k], acc[k]);
+    }
+    V<T>::store(Y + t * K + i * N, acc);
+  }
+}
+
+// The gradient of the combine: d_rows[p] = w[t, j] dY[t] and d_weights[t, j] = <dY[t], rows[p]>,
+// p = position[t, j]; a dropped choice has d_weights 0.  Eight choices at a time, their dot products
+// in registers; a token's threads add them up in a fixed order.
+constexpr int kBackTop = 8;
+template <typename T, template <typename> class V>
+__global__ void __launch_bounds__(kRowThreads)
+    expert_combine_backward_kernel(const T* __restrict__ dY, const T* __restrict__ rows, int64_t nrows, int64_t K,
+                                   const int* __restrict__ position, const float* __restrict__ weights, int64_t tokens,
+                                   int top, int tpt, T* __restrict__ d_rows, float* __restrict__ d_weights) {
+  constexpr int N = V<T>::kN;
+  __shared__ float part[kRowThreads / 32][kBackTop];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
+  const bool live = t < tokens;  // all threads stay for the barriers
+  const int64_t vectors = live ? K / N : 0;
+  for (int j0 = 0; j0 < top; j0 += kBackTop) {
+    const int nj = min(kBackTop, top - j0);
+    int p[kBackTop];
+    float w[kBackTop], dot[kBackTop];
+#pragma unroll
+    for (int j = 0; j < kBackTop; ++j) {
+      p[j] = live && j < nj ? __ldg(position + t * top + j0 + j) : -1;
+      if (p[j] >= nrows) p[j] = -1;
+      w[j] = p[j] >= 0 ? __ldg(weights + t * top + j0 + j) : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
+      float g[N];
+      V<T>::load(dY + t * K + i * N, g);
+#pragma unroll
+      for (int j = 0; j < kBackTop; ++j) {
+        if (p[j] < 0) continue;
+        const int64_t at = static_cast<int64_t>(p[j]) * K + i * N;
+        float z[N], d[N];
+        V<T>::load(rows + at, z);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          dot[j] = fmaf(g[k], z[k], dot[j]);
+          d[k] = w[j] * g[k];
+        }
+        V<T>::store(d_rows + at, d);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBackTop; ++j) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], off);
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int j = 0; j < kBackTop; ++j) part[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if (live && threadIdx.x % tpt < nj) {
+      const int j = threadIdx.x % tpt;
+      float sum = 0.f;
+      for (int k = 0; k < tpt / 32; ++k) sum += part[warp + k][j];
+      d_weights[t * top + j0 + j] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+static bool rows_vec(int64_t row_bytes, const void* a, const void* b, const void* c = nullptr, const void* d = nullptr) {
+  return row_bytes % 16 == 0 && aligned(a, 16) && aligned(b, 16) && aligned(c, 16) && aligned(d, 16);
+}
+
+struct RowGrid {
+  int tpt;
+  unsigned ctas;
+};
+static RowGrid row_grid(int64_t tokens, int64_t vectors) {
+  const int tpt = row_threads(vectors);
+  return {tpt, static_cast<unsigned>(ceil_div(tokens, kRowThreads / tpt))};
+}
+
+template <typename T, template <typename> class V>
+static void dispatch_as(const void* X, int64_t tokens, int64_t K, const int* position, int64_t top, void* out,
+                        cudaStream_t s) {
+  const RowGrid g = row_grid(tokens, K / V<T>::kN);
+  expert_dispatch_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(static_cast<const T*>(X), tokens, K, position,
+                                                              static_cast<int>(top), tokens * top, g.tpt,
+                                                              static_cast<T*>(out));
+}
+
+template <typename T>
+static void dispatch_typed(const void* X, int64_t tokens, int64_t K, const int* position, int64_t top, void* out,
+                           cudaStream_t s) {
+  if (rows_vec(K * sizeof(T), X, out))
+    dispatch_as<T, Vec>(X, tokens, K, position, top, out, s);
+  else
+    dispatch_as<T, One>(X, tokens, K, position, top, out, s);
+}
+
+hq_status launch_expert_dispatch(const void* X, int x_dtype, int64_t tokens, int64_t K, const int* position, int64_t top,
+                                 void* out, cudaStream_t s) {
+  if (x_dtype == HQ_BF16)
+    dispatch_typed<__nv_bfloat16>(X, tokens, K, position, top, out, s);
+  else
+    dispatch_typed<float>(X, tokens, K, position, top, out, s);
+  HQ_LAUNCH_CHECK();
+  return HQ_OK;
+}
+
+hq_status launch_expert_dispatch_fp8(const void* X, int x_dtype, int64_t tokens, int64_t K, const int* position,
+                                     int64_t top, uint8_t* codes, float* scales, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(tokens, 8)), static_cast<unsigned>(ceil_div(K, 512)));
+  const int64_t rows = tokens * top;
+  const int n = static_cast<int>(top);
+  if (x_dtype == HQ_BF16)
+    expert_dispatch_fp8_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(X), tokens, K, fp8_pitch(K), aligned(X, 16) && K % 8 == 0, position, n, rows,
+        codes, scales);
+  else
+    expert_dispatch_fp8_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(X), tokens, K, fp8_pitch(K),
+                                                           aligned(X, 16) && K % 4 == 0, position, n, rows, codes,
+                                                           scales);
+  HQ_LAUNCH_CHECK();
+  return HQ_OK;
+}
+
+template <typename T, template <typename> class V>
+static void combine_as(const void* rows, int64_t K, const int* position, const float* weights, int64_t tokens,
+                       int64_t top, void* Y, cudaStream_t s) {
+  const RowGrid g = row_grid(tokens, K / V<T>::kN);
+  expert_combine_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(static_cast<const T*>(rows), tokens * top, K, position,
+                                                             weights, tokens, static_cast<int>(top), g.tpt,
+                                                             static_cast<T*>(Y));
+}
+
+template <typename T>
+static void combine_typed(const void* rows, int64_t K, const int* position, const float* weights, int64_t tokens,
+                          int64_t top, void* Y, cudaStream_t s) {
+  if (rows_vec(K * sizeof(T), rows, Y))
+    combine_as<T, Vec>(rows, K, position, weights, tokens, top, Y, s);
+  else
+    combine_as<T, One>(rows, K, position, weights, tokens, top, Y, s);
+}
+
+hq_status launch_expert_combine(const void* rows, int dtype, int64_t tokens, int64_t K, const int* position, int64_t top,
+                                const float* weights, void* Y, cudaStream_t s) {
+  if (dtype == HQ_BF16)
+    combine_typed<__nv_bfloat16>(rows, K, position, weights, tokens, top, Y, s);
+  else
+    combine_typed<float>(rows, K, position, weights, tokens, top, Y, s);
+  HQ_LAUNCH_CHECK();
+  return HQ_OK;
+}
+
+template <typename T, template <typename> class V>
+static void combine_backward_as(const void* dY, const void* rows, int64_t K, const int* position, const float* weights,
+                                int64_t tokens, int64_t top, void* d_rows, float* d_weights, cudaStream_t s) {
+  const RowGrid g = row_grid(tokens, K / V<T>::kN);
+  expert_combine_backward_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(
+      static_cast<const T*>(dY), static_cast<const T*>(rows), tokens * top, K, position, weights, tokens,
+      static_cast<int>(top), g.tpt, static_cast<T*>(d_rows), d_weights);
+}
+
+template <typename T>
+static void combine_backward_typed(const void* dY, const void* rows, int64_t K, const int* position,
+                                   const float* weights, int64_t tokens, int64_t top, void* d_rows, float* d_weights,
+                                   cudaStream_t s) {
+  if (rows_vec(K * sizeof(T), dY, rows, d_rows))
+    combine_backward_as<T, Vec>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
+  else
+    combine_backward_as<T, One>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
+}
+
+hq_status launch_expert_combine_backward(const void* dY, const void* rows, int dtype, int64_t tokens, int64_t K,
+                                         const int* position, int64_t top, const float* weights, void* d_rows,
+                                         float* d_weights, cudaStream_t s) {
+  if (dtype == HQ_BF16)
+    combine_backward_typed<__nv_bfloat16>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
+  else
+    combine_backward_typed<float>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
+  HQ_LAUNCH_CHECK();
+  return HQ_OK;
+}
+
+}  // namespace hq

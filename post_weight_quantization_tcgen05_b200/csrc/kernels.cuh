@@ -195,6 +195,43 @@ size_t rtn_workspace(int64_t N, int64_t K, int64_t group);
 hq_status launch_rtn(const void* W, int w_dtype, int64_t N, int64_t K, int64_t group, const float* imp,
                      uint8_t* codes, float* scales, double* qerr_dev, uint8_t* ws, cudaStream_t s);
 
+// fp8_quant.cu: e4m3 codes (rows padded to 16 bytes) and block scales
+hq_status launch_fp8_rows(const void* X, int x_dtype, int64_t M, int64_t K, uint8_t* codes, float* scales,
+                          cudaStream_t s);
+hq_status launch_fp8_blocks(const void* W, int w_dtype, int64_t E, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                            cudaStream_t s);
+
+// fp8_gemm.cu: Y = A W^T on e4m3 codes with block scales; offsets (device, [E + 1]): rows
+// offsets[e] .. offsets[e + 1] - 1 meet matrix e; NULL: E = 1 and all rows
+struct Fp8Gemm {
+  const uint8_t* a_codes;
+  const float* a_scales;
+  int64_t rows;
+  const int* offsets;
+  const uint8_t* w_codes;
+  const float* w_scales;
+  int64_t E, N, K;
+  void* Y;
+  int y_dtype;
+  int* status;
+};
+hq_status launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s);
+
+// experts.cu: R = T top choices; see there
+constexpr int kMaxExperts = 1024;
+size_t expert_sort_workspace(int64_t R, int64_t E);
+hq_status launch_expert_sort(const int* ids, int64_t R, int64_t E, int* offsets, int* order, int* position,
+                             uint8_t* ws, cudaStream_t s);
+hq_status launch_expert_dispatch(const void* X, int x_dtype, int64_t tokens, int64_t K, const int* position, int64_t top,
+                                 void* out, cudaStream_t s);
+hq_status launch_expert_dispatch_fp8(const void* X, int x_dtype, int64_t tokens, int64_t K, const int* position,
+                                     int64_t top, uint8_t* codes, float* scales, cudaStream_t s);
+hq_status launch_expert_combine(const void* rows, int dtype, int64_t tokens, int64_t K, const int* position, int64_t top,
+                                const float* weights, void* Y, cudaStream_t s);
+hq_status launch_expert_combine_backward(const void* dY, const void* rows, int dtype, int64_t tokens, int64_t K,
+                                         const int* position, int64_t top, const float* weights, void* d_rows,
+                                         float* d_weights, cudaStream_t s);
+
 // gptq.cu: qerr reduction shared by GPTQ and RTN
 // (finfo: optional device int copied into hdr->info, the factorisation's status)
 hq_status launch_qerr_finalize(const double* partials, int64_t count, WsHeader* hdr, double* qerr_dev,

@@ -142,6 +142,17 @@ __device__ __forceinline__ void mma_tf32(uint32_t tmem_d, uint64_t adesc, uint64
       : "memory");
 }
 
+// Same with kind::f8f6f4 (e4m3 operands here), fp32 accumulate; one instruction takes 32 columns.
+__device__ __forceinline__ void mma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrives once on `bar` when every tcgen05.mma issued so far by this thread has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -221,8 +232,8 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
   return d;
 }
 
-// Instruction descriptor, kind::f16 / kind::tf32: D fp32 (bits 4-5 = 1), A/B format in bits
-// 7-9 / 10-12 (bf16 = 1, tf32 = 2), A/B MN-major flags in bits 15 / 16, N>>3 in bits 17-22,
+// Instruction descriptor, kind::f16 / kind::tf32 / kind::f8f6f4: D fp32 (bits 4-5 = 1), A/B format
+// in bits 7-9 / 10-12 (bf16 = 1, tf32 = 2, e4m3 = 0), A/B MN-major flags in bits 15 / 16, N>>3 in bits 17-22,
 // M>>4 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc(uint32_t ab_format, int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (ab_format << 7) | (ab_format << 10) | ((a_mn_major ? 1u : 0u) << 15) |
@@ -231,6 +242,7 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t ab_format, int M, int N, b
 }
 constexpr uint32_t kFmtBF16 = 1;
 constexpr uint32_t kFmtTF32 = 2;
+constexpr uint32_t kFmtE4M3 = 0;
 
 }  // namespace ptx
 }  // namespace hq
