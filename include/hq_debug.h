@@ -42,6 +42,14 @@ hq_status hq_debug_hessian_accumulate_impl(float* H, const void* X, int x_dtype,
                                            int* dev_status, int impl, hq_stream_t stream);
 
 /*
+ * hq_fp8_gemm (offsets NULL, E = 1) and hq_fp8_expert_gemm with an explicit kernel choice: impl
+ * 0 = automatic, 1 = one CTA per tile, 2 = a pair of CTAs per tile.
+ */
+hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
+                                 const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K,
+                                 void* Y, int y_dtype, int* dev_status, int impl, hq_stream_t stream);
+
+/*
  * The failure path of the tensor-core SYRK's bounded waits, made to run on purpose (no
  * counterpart on the pages; the library's rule that a device-side wait never hangs).  The
  * tcgen05 SYRK of hq_hessian_accumulate on bf16 X with

@@ -89,6 +89,7 @@ _SIGS = {
     "hq_fp8_linear_workspace_bytes": (_sz, [_i64, _i64]),
     "hq_fp8_linear": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _i64, _vp, _int, _vp, _sz, _vp, _vp]),
     "hq_fp8_expert_gemm": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _vp]),
+    "hq_debug_fp8_gemm_impl": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _int, _vp]),
     "hq_expert_sort_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "hq_expert_sort": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
     "hq_expert_dispatch": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp]),
@@ -554,6 +555,15 @@ def hq_fp8_expert_gemm(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y,
     a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
     _check(lib.hq_fp8_expert_gemm(a, sa, rows, off, w, sw, E, N, K, y, _dtype(Y), st, _stream(stream)),
            "hq_fp8_expert_gemm")
+
+
+def hq_debug_fp8_gemm_impl(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y, impl: int, dev_status=None,
+                           stream=None) -> None:
+    """hq_fp8_gemm (offsets None) or hq_fp8_expert_gemm by a chosen kernel (hq_debug.h)."""
+    rows, N = Y.shape
+    a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
+    _check(lib.hq_debug_fp8_gemm_impl(a, sa, rows, off, w, sw, 1 if offsets is None else w_codes.shape[0], N, K, y,
+                                      _dtype(Y), st, int(impl), _stream(stream)), "hq_debug_fp8_gemm_impl")
 
 
 def hq_expert_sort_workspace_bytes(T: int, top: int, E: int) -> int:

@@ -516,7 +516,7 @@ hq_status hq_fp8_gemm(const uint8_t* a_codes, const float* a_scales, int64_t M, 
   const Fp8Gemm g{a_codes, a_scales, M, nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status};
   const hq_status st = check_fp8_gemm(g);
   if (st != HQ_OK || M == 0) return st;
-  return launch_fp8_gemm(g, static_cast<cudaStream_t>(stream));
+  return launch_fp8_gemm(g, kFp8Auto, static_cast<cudaStream_t>(stream));
 }
 
 size_t hq_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
@@ -540,7 +540,7 @@ hq_status hq_fp8_linear(const void* X, int x_dtype, int64_t M, const uint8_t* w_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = launch_fp8_rows(X, x_dtype, M, K, codes, const_cast<float*>(g.a_scales), s);
   if (st != HQ_OK) return st;
-  return launch_fp8_gemm(g, s);
+  return launch_fp8_gemm(g, kFp8Auto, s);
 }
 
 hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
@@ -550,7 +550,17 @@ hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int6
   const hq_status st = check_fp8_gemm(g);
   if (st != HQ_OK || rows == 0) return st;
   if (offsets == nullptr || !aligned(offsets, 4)) return HQ_ERR_INVALID;
-  return launch_fp8_gemm(g, static_cast<cudaStream_t>(stream));
+  return launch_fp8_gemm(g, kFp8Auto, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
+                                 const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K,
+                                 void* Y, int y_dtype, int* dev_status, int impl, hq_stream_t stream) {
+  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status};
+  const hq_status st = check_fp8_gemm(g);
+  if (st != HQ_OK || rows == 0) return st;
+  if (impl < kFp8Auto || impl > kFp8Pair || (offsets == nullptr && E != 1)) return HQ_ERR_INVALID;
+  return launch_fp8_gemm(g, impl, static_cast<cudaStream_t>(stream));
 }
 
 size_t hq_expert_sort_workspace_bytes(int64_t T, int64_t top, int64_t E) {

@@ -8,15 +8,27 @@
 // registers.  So the accumulator restarts at every block, and the epilogue warps read and scale
 // one while the tensor core fills the other (two accumulators).
 //
-// One CTA per SM walks 128 x 128 tiles of Y; warp 0 loads 128 x 128 e4m3 boxes of A and W by TMA
-// (128-byte swizzle, K-major) into a ring of 32 KB stages, one stage per scale block; warp 1 issues
-// the MMAs; warps 2-9 (two per TMEM lane quadrant, 64 columns each) scale, add and store.  Columns
-// at and past K read as zeros (the tensor map's extent is K, not the row pitch), as do rows past
-// the operands' ends.  A tile of an expert that ends inside it computes rows of the next expert as
-// well (against the wrong matrix) and does not store them.
+// Two tilings of one kernel:
+//   pair   : two CTAs (a cluster) compute a 256 x 256 tile with cta_group::2 MMAs, each of them 128
+//            rows.  On one SM a 128 x 256 tile takes 48 KB of operands for every 512 cycles of
+//            tensor work, more than L2 gives all SMs at once; in a pair each CTA loads its 128 rows
+//            of A and half of the 256 rows of W, 32 KB, and the tensor cores read the other half
+//            from the peer's shared memory.  For many rows.
+//   single : one CTA, a 128 x 128 tile.  For few rows, where the tile's height is mostly padding and
+//            more, smaller tiles keep more SMs at work.
+//
+// One CTA per SM walks its tiles.  Warp 0 loads the operands by TMA (128 x 128 e4m3 boxes of A and W,
+// 128-byte swizzle, K-major) into a ring of 32 KB stages, one stage per scale block; warp 1 issues
+// the MMAs (in a pair, the even CTA's for both); warp 2 fetches the scales some blocks ahead and
+// leaves their products, and each tile's place, in shared memory; warps 4-11 (two per TMEM lane
+// quadrant, half of the tile's columns each) scale, add and store.  Columns at and past K read as
+// zeros (the tensor map's extent is K, not the row pitch), as do rows past the operands' ends.  A
+// tile of an expert that ends inside it computes rows of the next expert as well (against the wrong
+// matrix) and does not store them.
 //
 // Every wait is bounded: on expiry the CTA records HQ_ERR_TIMEOUT, waits (bounded) for its
-// in-flight TMA and MMA work, frees TMEM and returns.
+// in-flight TMA and MMA work, frees TMEM and returns; the CTAs of a pair meet at the end, so that
+// neither leaves while the other may still signal into its shared memory.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -28,13 +40,49 @@
 namespace hq {
 namespace {
 
-constexpr int kBM = 128, kBN = 128, kBK = kFp8Block;
-constexpr int kStages = 6;
-constexpr int kStageBytes = (kBM + kBN) * kBK;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kSMs = 148;
-constexpr int kBand = 16;  // tile rows of a band (the order of the tiles)
+constexpr int kBK = kFp8Block;  // columns of a pipeline stage: one scale block
+constexpr int kRows = 128;      // rows of A, and of W, that one CTA loads for a stage
+constexpr int kStages = 4;
+constexpr int kStageBytes = 2 * kRows * kBK;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kBand = 16;       // tile rows of a band (the order of the tiles)
+// Blocks whose scales are kept.  The epilogue gives them back by halves of the ring (one arrival of a
+// warp for every kScales / 2 blocks).
+constexpr int kScales = 8, kScaleHalf = kScales / 2;
+constexpr int kFetch = 4;  // blocks that the loads of the scales run ahead of their writes
+// Tiles whose places are kept: the scales are at most kScales blocks ahead of the epilogue, their loads
+// kFetch more, and every block may be another tile's.
+constexpr int kPlaces = 16;
+static_assert(kPlaces > kScales + kFetch, "a tile's place is overwritten after the epilogue read it");
+constexpr int kStoreBytes = 2 * 32 * 128;  // a warp's staging of output rows: two pieces of 32 x 128 bytes
+
+// Shared memory after the stages and the staging (both 1024-byte aligned).
+struct Tile {
+  int e, m0, m1, n0;  // expert, rows m0 .. m1 - 1, first column
+};
+struct Shared {
+  float scales[kScales][2][kRows];  // by half of the tile's columns, by row
+  Tile places[kPlaces];
+  uint64_t full[kStages];   // in a pair the even CTA's: both CTAs' loads
+  uint64_t empty[kStages];
+  uint64_t accf[2];         // accumulator filled
+  uint64_t acce[2];         // accumulator drained (in a pair the even CTA's: by both)
+  uint64_t scf[kScales];    // scales written
+  uint64_t sce[2];          // scales of half the ring read
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int start[kMaxExperts + 1];  // row tiles before each expert
+};
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kStoreBytes + 1024 /*align*/ + static_cast<int>(sizeof(Shared));
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+// Registers of the pair: 384 threads launch with 168 each; the epilogue's 256 hold 128 sums each and
+// take 216, the other 128 keep 72: 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsEpi = 216, kRegsCtl = 72;
+static_assert(kEpiWarps * 32 * kRegsEpi + 128 * kRegsCtl <= kThreads * kRegsLaunch, "register split");
 
 struct GemmArgs {
   void* Y;
@@ -45,11 +93,12 @@ struct GemmArgs {
   const float* w_scales;  // [E][nblocks][kblocks]
   const int* offsets;     // [E + 1] row ranges of the experts (NULL: one matrix for all rows)
   int E;
+  int y_aligned;          // rows of Y are 16-byte aligned (its tensor map is valid)
   int* status;
 };
 
-// Row tiles before each expert: start[e], with start[E] the total.  Offsets are device data: a
-// range outside [0, rows] is cut to it and an inverted one is empty, so no row index leaves Y.
+// An expert's rows.  Offsets are device data: a range outside [0, rows] is cut to it and an inverted
+// one is empty, so no row index leaves Y.
 __device__ __forceinline__ void expert_range(const GemmArgs& a, int e, int& r0, int& r1) {
   if (a.offsets == nullptr) {
     r0 = 0;
@@ -60,12 +109,13 @@ __device__ __forceinline__ void expert_range(const GemmArgs& a, int e, int& r0, 
   r1 = min(max(a.offsets[e + 1], r0), a.rows);
 }
 
-// All threads: fills start[0 .. E].
+// All threads: fills start[0 .. E] with tiles of BM rows; valid after the next barrier.
+template <int BM>
 __device__ __forceinline__ void expert_tiles(const GemmArgs& a, int* start) {
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     int r0, r1;
     expert_range(a, e, r0, r1);
-    start[e + 1] = (r1 - r0 + kBM - 1) / kBM;
+    start[e + 1] = (r1 - r0 + BM - 1) / BM;
   }
   if (threadIdx.x == 0) start[0] = 0;
   __syncthreads();
@@ -86,17 +136,14 @@ __device__ __forceinline__ void expert_tiles(const GemmArgs& a, int* start) {
   }
 }
 
-struct Tile {
-  int e, m0, m1, n0;  // expert, its rows m0 .. m1 - 1 of this tile, first column
-};
-
-// Tiles in bands of kBand row tiles, inside a band column by column, so that the tiles in flight
+// Tile t, in bands of kBand row tiles, inside a band column by column, so that the tiles in flight
 // share their operands through L2.
-__device__ __forceinline__ Tile tile_at(const GemmArgs& a, const int* start, int tiles_n, int64_t t) {
-  const int tiles_m = start[a.E];
-  const int64_t per_band = static_cast<int64_t>(kBand) * tiles_n;
-  const int band = static_cast<int>(t / per_band);
-  const int in_band = static_cast<int>(t - band * per_band);
+template <int BM, int BN>
+__device__ __forceinline__ Tile tile_at(const GemmArgs& a, const int* start, int t) {
+  const int tiles_m = start[a.E], tiles_n = (a.N + BN - 1) / BN;
+  const int per_band = kBand * tiles_n;
+  const int band = t / per_band;
+  const int in_band = t - band * per_band;
   const int h = min(kBand, tiles_m - band * kBand);
   const int mt = band * kBand + in_band % h;
   int lo = 0, hi = a.E - 1;  // the last expert whose first row tile is at or before mt
@@ -113,248 +160,405 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, const int* start, int
   expert_range(a, lo, r0, r1);
   Tile x;
   x.e = lo;
-  x.m0 = r0 + (mt - start[lo]) * kBM;
-  x.m1 = min(r1, x.m0 + kBM);
-  x.n0 = in_band / h * kBN;
+  x.m0 = r0 + (mt - start[lo]) * BM;
+  x.m1 = min(r1, x.m0 + BM);
+  x.n0 = in_band / h * BN;
   return x;
 }
 
-template <typename TY>
-__device__ __forceinline__ void store_row(TY* y, int col, int N, bool vec, const float (&acc)[64]);
-
-template <>
-__device__ __forceinline__ void store_row<float>(float* y, int col, int N, bool vec, const float (&acc)[64]) {
+// 16 bytes of output from fp32 sums.
+__device__ __forceinline__ uint4 pack16(const float* v, float) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack16(const float* v, __nv_bfloat16) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 64; i += 4) {
-    if (vec && col + i + 4 <= N) {
-      *reinterpret_cast<float4*>(y + col + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (col + i + k < N) y[col + i + k] = acc[i + k];
-    }
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <>
-__device__ __forceinline__ void store_row<__nv_bfloat16>(__nv_bfloat16* y, int col, int N, bool vec,
-                                                         const float (&acc)[64]) {
+// A warp's 32 rows x NC columns of Y, one row of sums a lane, through shared memory of its own in
+// pieces of 32 rows x 128 bytes: a lane's own row would go out as 16-byte pieces of 32 different lines
+// (measured 10,000 cycles for a 128 x 256 tile, the time of eleven blocks of the product).  A whole
+// piece leaves by a TMA store, which runs on while the warp takes up the next tile; one that an
+// expert's last row cuts, or unaligned rows of Y, by stores of the lanes, 8 a row.  16-byte part p of
+// row r is kept at place p ^ (r % 8), the 128-byte swizzle of the tensor map.  Rows from `rows_left`
+// on and columns from N on are not written.
+template <int NC, typename TY>
+__device__ __forceinline__ void store_rows(const GemmArgs& a, const CUtensorMap* map, uint8_t* stage, int row, int col,
+                                           int rows_left, const float (&acc)[NC], int lane, int& turn) {
+  constexpr int kPer = 16 / sizeof(TY);  // columns of 16 bytes
+  constexpr int kPiece = 8 * kPer;       // columns of a piece
+  constexpr int kPieces = NC / kPiece;
+  if (rows_left <= 0 || col >= a.N) return;
+  const bool whole = a.y_aligned && rows_left >= 32;
+  (void)HQ_IN_BOUNDS(row >= 0 && row + min(rows_left, 32) <= a.rows);
 #pragma unroll
-  for (int i = 0; i < 64; i += 8) {
-    if (vec && col + i + 8 <= N) {
-      uint32_t w[4];
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = i * kPiece;
+    uint8_t* buf = stage + (turn++ & 1) * (32 * 128);  // two pieces take turns, across tiles too
+    // the piece before the last, which lay here, has been read by its store
+    if (lane == 0) ptx::bulk_wait_read<1>();
+    __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[i + 2 * k], acc[i + 2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int p = 0; p < 8; ++p)
+      *reinterpret_cast<uint4*>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = pack16(acc + c + p * kPer, TY());
+    if (whole) {
+      ptx::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (col + c < a.N) ptx::tma_store_2d(map, buf, col + c, row);
+        ptx::bulk_commit();
       }
-      *reinterpret_cast<uint4*>(y + col + i) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
+      __syncwarp();
+      const int p = lane & 7;
+      const int at = col + c + p * kPer;
+      for (int r = lane >> 3; r < 32 && r < rows_left; r += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) << 4));
+        TY* out = static_cast<TY*>(a.Y) + static_cast<int64_t>(row + r) * a.N + at;
+        if (a.y_aligned && at + kPer <= a.N) {
+          *reinterpret_cast<uint4*>(out) = v;
+        } else {
+          const TY* e = reinterpret_cast<const TY*>(&v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (col + i + k < N) y[col + i + k] = __float2bfloat16_rn(acc[i + k]);
+          for (int k = 0; k < kPer; ++k)
+            if (at + k < a.N) out[k] = e[k];
+        }
+      }
+      if (lane == 0) ptx::bulk_commit();  // an empty group in the store's place
     }
   }
 }
 
-constexpr int kSmem = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/ + (kMaxExperts + 1) * 4;
-
-template <typename TY>
+template <bool kPair, typename TY>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW, GemmArgs args) {
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW,
+                    const __grid_constant__ CUtensorMap mapY, GemmArgs args) {
+  constexpr int kBM = kPair ? 256 : 128, kBN = kPair ? 256 : 128;  // the tile
+  constexpr int NC = kBN / 2;                                      // columns of an epilogue warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* accf = empty + kStages;  // [2] accumulator filled
-  uint64_t* acce = accf + 2;         // [2] accumulator drained
-  uint64_t* drain = acce + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* start = reinterpret_cast<int*>(smem + kStages * kStageBytes + 256);
+  uint8_t* stores = smem + kStages * kStageBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(stores + kEpiWarps * kStoreBytes);
+  volatile int* abort_flag = &sh.abort;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(ptx::cluster_ctarank()) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
+      ptx::mbar_init(&sh.full[s], 1);
+      ptx::mbar_init(&sh.empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      ptx::mbar_init(&accf[a], 1);
-      ptx::mbar_init(&acce[a], kEpiWarps);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&sh.accf[b], 1);
+      ptx::mbar_init(&sh.acce[b], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
-    ptx::mbar_init(drain, 1);
-    *abort_flag = 0;
+    for (int s = 0; s < kScales; ++s) ptx::mbar_init(&sh.scf[s], 1);
+    for (int s = 0; s < 2; ++s) ptx::mbar_init(&sh.sce[s], kEpiWarps);
+    ptx::mbar_init(&sh.drain, 1);
+    sh.abort = 0;
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, 2 * kBN);
-    ptx::tmem_relinquish();
+    if constexpr (kPair) {
+      ptx::tmem_alloc_pair(&sh.tmem, 2 * kBN);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(&sh.tmem, 2 * kBN);
+      ptx::tmem_relinquish();
+    }
   }
-  expert_tiles(args, start);
+  expert_tiles<kBM>(args, sh.start);
   ptx::tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) ptx::cluster_sync();  // the peer's barriers exist before anything signals them
   ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int tiles_n = (args.N + kBN - 1) / kBN;
-  const int64_t tiles = static_cast<int64_t>(start[args.E]) * tiles_n;
+  const uint32_t tmem = sh.tmem;
+  const int tiles = sh.start[args.E] * ((args.N + kBN - 1) / kBN);
+  const int first = kPair ? blockIdx.x >> 1 : blockIdx.x, step = kPair ? gridDim.x >> 1 : gridDim.x;
+  const int own = tiles > first ? (tiles - 1 - first) / step + 1 : 0;  // tiles of this CTA (or pair)
+  const int blocks = own * args.kblocks;  // their blocks follow one another across tiles
 
   auto fail = [&]() {
     *abort_flag = 1;
     record_status(args.status, HQ_ERR_TIMEOUT);
   };
-
+  if (warp < 4) {
+    if constexpr (kPair) ptx::regs_dec<kRegsCtl>();
+  }
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
     ptx::prefetch_tensormap(&mapA);
     ptx::prefetch_tensormap(&mapW);
     int g = 0;  // stages issued by this CTA
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at(args, start, tiles_n, t);
-      const int w_row = x.e * args.N + x.n0;
+    for (int i = 0; i < own && ok; ++i) {
+      const Tile x = tile_at<kBM, kBN>(args, sh.start, first + i * step);
+      const int a_row = x.m0 + rank * kRows;
+      const int w_row = x.e * args.N + x.n0 + rank * kRows;
+      (void)HQ_IN_BOUNDS(x.m0 < args.rows && x.n0 < args.N);
       for (int k = 0; k < args.kblocks; ++k, ++g) {
         const int s = g % kStages;
-        if (g >= kStages && !ptx::mbar_wait(&empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
+        if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
         uint8_t* sa = smem + s * kStageBytes;
-        (void)HQ_IN_BOUNDS(x.m0 < args.rows && x.n0 < args.N && k * kBK < args.K);
-        ptx::mbar_arrive_expect_tx(&full[s], kStageBytes);
-        ptx::tma_load_2d(sa, &mapA, k * kBK, x.m0, &full[s]);
-        ptx::tma_load_2d(sa + kBM * kBK, &mapW, k * kBK, w_row, &full[s]);
+        if constexpr (kPair) {
+          // the even CTA announces both CTAs' bytes; the odd one's may arrive before that, the phase
+          // completes only after it
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
+          const uint32_t bar = ptx::mapa(&sh.full[s], 0);
+          ptx::tma_load_2d_pair(sa, &mapA, k * kBK, a_row, bar);
+          ptx::tma_load_2d_pair(sa + kRows * kBK, &mapW, k * kBK, w_row, bar);
+        } else {
+          ptx::mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
+          ptx::tma_load_2d(sa, &mapA, k * kBK, a_row, &sh.full[s]);
+          ptx::tma_load_2d(sa + kRows * kBK, &mapW, k * kBK, w_row, &sh.full[s]);
+        }
       }
     }
     if (!ok) {
       fail();
-      // let the copies already issued land before the CTA's shared memory goes away
-      const int first = g > kStages ? g - kStages : 0;
-      for (int k = first; k < g; ++k) ptx::mbar_wait(&full[k % kStages], (k / kStages) & 1, nullptr);
+      // let the copies already issued land before shared memory goes away
+      if (rank == 0)
+        for (int k = g > kStages ? g - kStages : 0; k < g; ++k)
+          ptx::mbar_wait(&sh.full[k % kStages], (k / kStages) & 1, nullptr);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kBM, kBN, false, false);
     bool ok = true;
-    int g = 0;  // blocks issued (stage g % kStages, accumulator g & 1)
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      for (int k = 0; k < args.kblocks; ++k, ++g) {
-        const int s = g % kStages, acc = g & 1;
-        if ((g >= 2 && !ptx::mbar_wait(&acce[acc], ((g >> 1) - 1) & 1, abort_flag)) ||
-            !ptx::mbar_wait(&full[s], (g / kStages) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t dacc = tmem + static_cast<uint32_t>(acc * kBN);
-        const uint32_t sa = ptx::smem_u32(smem + s * kStageBytes);
-        const uint32_t sb = sa + kBM * kBK;
+    for (int g = 0; g < blocks; ++g) {
+      const int s = g % kStages, b = g & 1;
+      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag) ||
+          (g >= 2 && !ptx::mbar_wait(&sh.acce[b], ((g >> 1) - 1) & 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t dacc = tmem + static_cast<uint32_t>(b * kBN);
+      const uint32_t sa = ptx::smem_u32(smem + s * kStageBytes);
+      const uint32_t sb = sa + kRows * kBK;
 #pragma unroll
-        for (int kk = 0; kk < kBK / 32; ++kk) {
-          // K-major rows of 128 bytes, 8-row groups 1 KB apart (SBO); an MMA takes 32 bytes of each row
-          const uint64_t ad = ptx::sdesc_sw128(sa + kk * 32, 16, 1024);
-          const uint64_t bd = ptx::sdesc_sw128(sb + kk * 32, 16, 1024);
+      for (int kk = 0; kk < kBK / 32; ++kk) {
+        // K-major rows of 128 bytes, 8-row groups 1 KB apart (SBO); an MMA takes 32 bytes of each row
+        const uint64_t ad = ptx::sdesc_sw128(sa + kk * 32, 16, 1024);
+        const uint64_t bd = ptx::sdesc_sw128(sb + kk * 32, 16, 1024);
+        if constexpr (kPair)
+          ptx::mma_f8_pair(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
+        else
           ptx::mma_f8(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
-        }
-        ptx::mma_commit(&empty[s]);
-        ptx::mma_commit(&accf[acc]);
+      }
+      if constexpr (kPair) {
+        ptx::mma_commit_pair(&sh.accf[b]);
+        ptx::mma_commit_pair(&sh.empty[s]);
+      } else {
+        ptx::mma_commit(&sh.accf[b]);
+        ptx::mma_commit(&sh.empty[s]);
       }
     }
     if (!ok) {
       fail();
-      ptx::mma_commit(drain);
-      ptx::mbar_wait(drain, 0, nullptr);
+      if constexpr (kPair)
+        ptx::mma_commit_pair(&sh.drain);
+      else
+        ptx::mma_commit(&sh.drain);
+      ptx::mbar_wait(&sh.drain, 0, nullptr);
     }
-  } else if (warp >= 2) {
-    // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;         // TMEM lane quadrant this warp may access
-    const int h = (warp - 2) >> 2;  // which 64-column half of the tile
-    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    const bool vec = (reinterpret_cast<uintptr_t>(args.Y) & 15) == 0 && (args.N * static_cast<int64_t>(sizeof(TY))) % 16 == 0;
-    bool ok = true;
-    int g = 0;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile x = tile_at(args, start, tiles_n, t);
-      const int row = x.m0 + q * 32 + lane;
-      const bool live = row < x.m1;
-      const float* sa = args.a_scales + row;  // + k * rows
-      const float* sw = args.w_scales + (static_cast<int64_t>(x.e) * args.nblocks + x.n0 / kFp8Block) * args.kblocks;
-      float acc[64];
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales
+    // A lane fetches the scales of 4 rows, kFetch blocks ahead of the block it writes.
+    float sa[kFetch][4], sw[kFetch][2];
+    Tile x{};
+    int k = args.kblocks, i = -1;  // the block to fetch: the first of the tile after tile i
+    auto fetch = [&](int f, int g) {
+      if (g >= blocks) return;
+      if (k == args.kblocks) {
+        k = 0;
+        ++i;
+        x = tile_at<kBM, kBN>(args, sh.start, first + i * step);
+        // its place is read by the epilogue after its first block's scales are announced, later
+        if (lane == 0) sh.places[i % kPlaces] = x;
+      }
+      const float* col = args.a_scales + static_cast<int64_t>(k) * args.rows;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+      for (int r = 0; r < 4; ++r) {
+        const int row = x.m0 + rank * kRows + r * 32 + lane;
+        sa[f][r] = row < x.m1 ? __ldg(col + row) : 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int nb = (x.n0 + h * NC) / kFp8Block;
+        sw[f][h] = nb < args.nblocks
+                       ? __ldg(args.w_scales + (static_cast<int64_t>(x.e) * args.nblocks + nb) * args.kblocks + k)
+                       : 0.f;
+      }
+      ++k;
+    };
+#pragma unroll
+    for (int f = 0; f < kFetch; ++f) fetch(f, f);
+    bool ok = true;
+    for (int g0 = 0; g0 < blocks && ok; g0 += kFetch) {
+#pragma unroll
+      for (int f = 0; f < kFetch; ++f) {
+        const int g = g0 + f;
+        if (g >= blocks || !ok) break;
+        if (g % kScaleHalf == 0 && g >= kScales)
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[(g / kScaleHalf) & 1], ((g / kScales) - 1) & 1, abort_flag));
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sh.scales[g % kScales][h][r * 32 + lane] = sa[f][r] * sw[f][h];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.scf[g % kScales]);
+        fetch(f, g + kFetch);
+      }
+    }
+    if (!ok) fail();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    if constexpr (kPair) ptx::regs_inc<kRegsEpi>();
+    // The time from "accumulator filled" to "drained" holds up the tensor core, as there are only two,
+    // so it contains the loads from tensor memory and no more of the sums than free the registers for
+    // them.  The last sums run while the next block's barriers are looked at.
+    const int q = warp & 3;         // TMEM lane quadrant this warp may access
+    const int h = (warp - 4) >> 2;  // which half of the tile's columns
+    const uint32_t tmem_w = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * NC);
+    uint8_t* stage = stores + (warp - 4) * kStoreBytes;
+    const uint32_t scale_at = ptx::smem_u32(&sh.scales[0][h][q * 32 + lane]);
+    bool ok = true, seen = false;  // seen: this block's barriers have been seen complete
+    int g = 0, turn = 0;
+    for (int i = 0; i < own && ok; ++i) {
+      float acc[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[c] = 0.f;
       for (int k = 0; k < args.kblocks; ++k, ++g) {
-        const float scale = live ? __ldg(sa + static_cast<int64_t>(k) * args.rows) * __ldg(sw + k) : 0.f;
         const int b = g & 1;
-        if (!ptx::mbar_wait(&accf[b], (g >> 1) & 1, abort_flag)) {
-          ok = false;
-          break;
+        if (!__all_sync(0xffffffffu, seen)) {
+          // the warp goes on or gives up as one: a wait may run out for some of its lanes only
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.scf[g % kScales], (g / kScales) & 1, abort_flag) &&
+                                           ptx::mbar_wait(&sh.accf[b], (g >> 1) & 1, abort_flag));
+          if (!ok) break;
         }
         ptx::tc_fence_after();
-        uint32_t r0[32], r1[32];
-        const uint32_t from = tmem + lane_off + static_cast<uint32_t>(b * kBN + h * 64);
-        ptx::tmem_ld32_nowait(from, r0);
-        ptx::tmem_ld32_nowait(from + 32, r1);
+        const uint32_t from = tmem_w + static_cast<uint32_t>(b * kBN);
+        uint32_t r[2][32];
+        ptx::tmem_ld32_nowait(from, r[0]);
+        ptx::tmem_ld32_nowait(from + 32, r[1]);
+        const float scale = ptx::lds32(scale_at + (g % kScales) * (2 * kRows * 4));
+        auto add = [&](int c) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            ptx::fma2(acc[32 * c + j], acc[32 * c + j + 1], scale, r[c & 1][j], r[c & 1][j + 1]);
+        };
         ptx::tmem_wait_ld();
+        if constexpr (NC == 128) {
+          add(0);
+          ptx::tmem_ld32_nowait(from + 64, r[0]);
+          add(1);
+          ptx::tmem_ld32_nowait(from + 96, r[1]);
+          ptx::tmem_wait_ld();
+        }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&acce[b]);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          acc[i] = fmaf(scale, __uint_as_float(r0[i]), acc[i]);
-          acc[32 + i] = fmaf(scale, __uint_as_float(r1[i]), acc[32 + i]);
+        if (lane == 0) {
+          if constexpr (kPair)
+            ptx::mbar_arrive_cluster(ptx::mapa(&sh.acce[b], 0));
+          else
+            ptx::mbar_arrive(&sh.acce[b]);
+          if (g % kScaleHalf == kScaleHalf - 1) ptx::mbar_arrive(&sh.sce[(g / kScaleHalf) & 1]);
         }
+        const int n = g + 1;
+        seen = n < blocks && ptx::mbar_try_wait(&sh.scf[n % kScales], (n / kScales) & 1) &&
+               ptx::mbar_try_wait(&sh.accf[n & 1], (n >> 1) & 1);
+        add(NC / 32 - 2);
+        add(NC / 32 - 1);
       }
-      if (ok && live && HQ_IN_BOUNDS(row >= 0 && row < args.rows))
-        store_row<TY>(static_cast<TY*>(args.Y) + static_cast<int64_t>(row) * args.N, x.n0 + h * 64, args.N, vec, acc);
+      if (!ok) break;
+      const Tile x = sh.places[i % kPlaces];
+      const int row = x.m0 + rank * kRows + q * 32;
+      store_rows<NC, TY>(args, &mapY, stage, row, x.n0 + h * NC, x.m1 - row, acc, lane, turn);
     }
+    if (lane == 0) ptx::bulk_wait<0>();
     if (!ok) fail();
   }
 
   ptx::tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 2 * kBN);
+    if constexpr (kPair)
+      ptx::tmem_dealloc_pair(tmem, 2 * kBN);
+    else
+      ptx::tmem_dealloc(tmem, 2 * kBN);
   }
 }
 
-template <typename TY>
+template <bool kPair, typename TY>
 hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
-  CUtensorMap map_a, map_w;
+  constexpr int kTile = kPair ? 256 : 128;
+  const int64_t kblocks = ceil_div(p.K, kFp8Block);
+  // an expert's rows may leave one partial row tile each
+  const int64_t most = (p.rows / kTile + (p.offsets != nullptr ? p.E : 1)) * ceil_div(p.N, kTile);
+  if (most * kblocks > 0x7FFFFFFF) return HQ_ERR_UNSUPPORTED;
   const uint64_t pitch = static_cast<uint64_t>(fp8_pitch(p.K));
+  CUtensorMap map_a, map_w, map_y;
   if (!make_tmap_2d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a_codes, static_cast<uint64_t>(p.K),
-                    static_cast<uint64_t>(p.rows), pitch, kBK, kBM) ||
+                    static_cast<uint64_t>(p.rows), pitch, kBK, kRows) ||
       !make_tmap_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w_codes, static_cast<uint64_t>(p.K),
-                    static_cast<uint64_t>(p.E * p.N), pitch, kBK, kBN))
+                    static_cast<uint64_t>(p.E * p.N), pitch, kBK, kRows))
     return HQ_ERR_CUDA;
-  HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   GemmArgs a{};
   a.Y = p.Y;
   a.rows = static_cast<int>(p.rows);
   a.N = static_cast<int>(p.N);
   a.K = static_cast<int>(p.K);
-  a.kblocks = static_cast<int>(ceil_div(p.K, kFp8Block));
+  a.kblocks = static_cast<int>(kblocks);
   a.nblocks = static_cast<int>(ceil_div(p.N, kFp8Block));
   a.a_scales = p.a_scales;
   a.w_scales = p.w_scales;
   a.offsets = p.offsets;
   a.E = static_cast<int>(p.E);
+  a.y_aligned = aligned(p.Y, 16) && p.N * sizeof(TY) % 16 == 0;
   a.status = p.status;
-  // an expert's rows may leave one partial row tile each
-  const int64_t most = (p.rows / kBM + (p.offsets != nullptr ? p.E : 1)) * ceil_div(p.N, kBN);
-  const int grid = static_cast<int>(most < kSMs ? most : kSMs);
-  fp8_gemm_kernel<TY><<<grid, kThreads, kSmem, s>>>(map_a, map_w, a);
-  HQ_LAUNCH_CHECK();
+  if (!a.y_aligned)
+    map_y = map_a;  // not used
+  else if (!make_tmap_2d(&map_y, sizeof(TY) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y,
+                         static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.rows), p.N * sizeof(TY), 128 / sizeof(TY), 32))
+    return HQ_ERR_CUDA;
+  HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<kPair, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  const int slots = kPair ? kSMs / 2 : kSMs;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * (kPair ? 2 : 1)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPair ? 2 : 1;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 1 : 0;
+  HQ_LAUNCH_CHAINED(cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<kPair, TY>, map_a, map_w, map_y, a));
   return HQ_OK;
 }
 
 }  // namespace
 
-hq_status launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s) {
+hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s) {
   if (p.rows == 0) return HQ_OK;
-  return p.y_dtype == HQ_F32 ? run_gemm<float>(p, s) : run_gemm<__nv_bfloat16>(p, s);
+  if (impl == kFp8Auto) impl = p.rows / p.E >= 256 ? kFp8Pair : kFp8Single;
+  if (impl == kFp8Pair) return p.y_dtype == HQ_F32 ? run_gemm<true, float>(p, s) : run_gemm<true, __nv_bfloat16>(p, s);
+  return p.y_dtype == HQ_F32 ? run_gemm<false, float>(p, s) : run_gemm<false, __nv_bfloat16>(p, s);
 }
 
 }  // namespace hq

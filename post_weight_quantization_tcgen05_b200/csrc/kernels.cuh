@@ -215,7 +215,8 @@ struct Fp8Gemm {
   int y_dtype;
   int* status;
 };
-hq_status launch_fp8_gemm(const Fp8Gemm& p, cudaStream_t s);
+enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2 };
+hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s);
 
 // experts.cu: R = T top choices; see there
 constexpr int kMaxExperts = 1024;

@@ -328,3 +328,47 @@ def test_linear_on_a_side_stream_and_in_a_graph(hq, cuda_device, M, N, K):
         x.copy_(src)
         graph.replay()
         assert torch.equal(Y, ref)
+
+
+# ------------------------------------------------------------------ the kernels one by one
+
+IMPLS = {"single": 1, "pair": 2}
+
+
+@pytest.mark.parametrize("impl", list(IMPLS))
+@pytest.mark.parametrize("M,N,K", SHAPES + [(2900, 3400, 400), (512, 17408, 256)])
+def test_every_kernel_on_one_weight(hq, cuda_device, M, N, K, impl):
+    a, sa = small_integers(1, M, K, 1)
+    w, sw = small_integers(2, N, K, 128)
+    sa = sa.t().contiguous()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ref = ((a[:, :K].double() * sa.double().t().repeat_interleave(128, 1)[:, :K])
+           @ (w[:, :K].double() * sw.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]).t())
+    for dt in ("f32", "bf16"):
+        Y = torch.full((M, N), float("nan"), dtype=TYPES[dt], device="cuda")
+        hq.hq_debug_fp8_gemm_impl(a, sa, None, w, sw, K, Y, IMPLS[impl], dev_status=status)
+        assert torch.equal(Y, ref.float().to(TYPES[dt]))
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("impl", list(IMPLS))
+@pytest.mark.parametrize("sizes,gaps,N,K", [([1], (0, 0), 64, 64), ([0, 5, 0, 0, 130, 1, 0], (0, 0), 130, 200),
+                                            ([3, 0, 300], (2, 5), 257, 300), ([0, 0, 0], (0, 7), 64, 64),
+                                            ([700, 2, 900], (1, 0), 384, 512), ([257, 0, 1, 255, 256] * 8, (0, 9), 640, 260)])
+def test_every_kernel_on_experts(hq, cuda_device, sizes, gaps, N, K, impl):
+    E = len(sizes)
+    offsets, rows = expert_case(0, sizes, gaps, N, K)
+    a, sa = small_integers(3, rows, K, 1)
+    w, sw = small_integers(4, E * N, K, N)  # one row of scales for each expert's N rows
+    sw = sw[:, None].expand(E, -(-N // 128), -1).contiguous()
+    Y = torch.full((rows, N), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hq.hq_debug_fp8_gemm_impl(a, sa.t().contiguous(), offsets, w.view(E, N, -1), sw, K, Y, IMPLS[impl], dev_status=status)
+    A = a[:, :K].double() * sa.double().repeat_interleave(128, 1)[:, :K]
+    ref = torch.full((rows, N), 7.0, dtype=torch.float64, device="cuda")
+    off = offsets.tolist()
+    for e in range(E):
+        W = w.view(E, N, -1)[e, :, :K].double() * sw[e, 0].double().repeat_interleave(128)[:K]
+        ref[off[e]:off[e + 1]] = A[off[e]:off[e + 1]] @ W.t()
+    assert torch.equal(Y.double(), ref)
+    assert status.item() == 0
