@@ -559,7 +559,7 @@ hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, 
   const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status};
   const hq_status st = check_fp8_gemm(g);
   if (st != HQ_OK || rows == 0) return st;
-  if (impl < kFp8Auto || impl > kFp8Pair || (offsets == nullptr && E != 1)) return HQ_ERR_INVALID;
+  if (impl < kFp8Auto || impl > kFp8Few64 || (offsets == nullptr && E != 1)) return HQ_ERR_INVALID;
   return launch_fp8_gemm(g, impl, static_cast<cudaStream_t>(stream));
 }
 

@@ -29,29 +29,20 @@
 // Every wait is bounded: on expiry the CTA records HQ_ERR_TIMEOUT, waits (bounded) for its
 // in-flight TMA and MMA work, frees TMEM and returns; the CTAs of a pair meet at the end, so that
 // neither leaves while the other may still signal into its shared memory.
-#include <cuda_bf16.h>
-
-#include "common.cuh"
-#include "fp8_quant.cuh"
-#include "kernels.cuh"
-#include "ptx.cuh"
-#include "tmap.cuh"
+#include "fp8_gemm.cuh"
 
 namespace hq {
+namespace fp8 {
 namespace {
 
-constexpr int kSMs = 148;
-constexpr int kBK = kFp8Block;  // columns of a pipeline stage: one scale block
 constexpr int kRows = 128;      // rows of A, and of W, that one CTA loads for a stage
 constexpr int kStages = 4;
 constexpr int kStageBytes = 2 * kRows * kBK;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kBand = 16;       // tile rows of a band (the order of the tiles)
-// Blocks whose scales are kept.  The epilogue gives them back by halves of the ring (one arrival of a
-// warp for every kScales / 2 blocks).
+// Blocks whose scales are kept.  They are handed over, and given back, by halves of the ring.
 constexpr int kScales = 8, kScaleHalf = kScales / 2;
-constexpr int kFetch = 4;  // blocks that the loads of the scales run ahead of their writes
+constexpr int kFetch = kScaleHalf;  // blocks that the loads of the scales run ahead of their writes
 // Tiles whose places are kept: the scales are at most kScales blocks ahead of the epilogue, their loads
 // kFetch more, and every block may be another tile's.
 constexpr int kPlaces = 16;
@@ -59,9 +50,6 @@ static_assert(kPlaces > kScales + kFetch, "a tile's place is overwritten after t
 constexpr int kStoreBytes = 2 * 32 * 128;  // a warp's staging of output rows: two pieces of 32 x 128 bytes
 
 // Shared memory after the stages and the staging (both 1024-byte aligned).
-struct Tile {
-  int e, m0, m1, n0;  // expert, rows m0 .. m1 - 1, first column
-};
 struct Shared {
   float scales[kScales][2][kRows];  // by half of the tile's columns, by row
   Tile places[kPlaces];
@@ -69,7 +57,7 @@ struct Shared {
   uint64_t empty[kStages];
   uint64_t accf[2];         // accumulator filled
   uint64_t acce[2];         // accumulator drained (in a pair the even CTA's: by both)
-  uint64_t scf[kScales];    // scales written
+  uint64_t scf[2];          // scales of half the ring written
   uint64_t sce[2];          // scales of half the ring read
   uint64_t drain;
   uint32_t tmem;
@@ -83,88 +71,6 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 // take 216, the other 128 keep 72: 256 * 216 + 128 * 72 = 384 * 168.
 constexpr int kRegsLaunch = 168, kRegsEpi = 216, kRegsCtl = 72;
 static_assert(kEpiWarps * 32 * kRegsEpi + 128 * kRegsCtl <= kThreads * kRegsLaunch, "register split");
-
-struct GemmArgs {
-  void* Y;
-  int rows;             // rows of A and Y
-  int N, K;
-  int kblocks, nblocks;  // ceil(K / 128), ceil(N / 128)
-  const float* a_scales;  // [kblocks][rows]
-  const float* w_scales;  // [E][nblocks][kblocks]
-  const int* offsets;     // [E + 1] row ranges of the experts (NULL: one matrix for all rows)
-  int E;
-  int y_aligned;          // rows of Y are 16-byte aligned (its tensor map is valid)
-  int* status;
-};
-
-// An expert's rows.  Offsets are device data: a range outside [0, rows] is cut to it and an inverted
-// one is empty, so no row index leaves Y.
-__device__ __forceinline__ void expert_range(const GemmArgs& a, int e, int& r0, int& r1) {
-  if (a.offsets == nullptr) {
-    r0 = 0;
-    r1 = a.rows;
-    return;
-  }
-  r0 = min(max(a.offsets[e], 0), a.rows);
-  r1 = min(max(a.offsets[e + 1], r0), a.rows);
-}
-
-// All threads: fills start[0 .. E] with tiles of BM rows; valid after the next barrier.
-template <int BM>
-__device__ __forceinline__ void expert_tiles(const GemmArgs& a, int* start) {
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    int r0, r1;
-    expert_range(a, e, r0, r1);
-    start[e + 1] = (r1 - r0 + BM - 1) / BM;
-  }
-  if (threadIdx.x == 0) start[0] = 0;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int per = (a.E + 31) / 32, e0 = threadIdx.x * per;
-    int sum = 0;
-    for (int e = e0; e < e0 + per && e < a.E; ++e) sum += start[e + 1];
-    int before = sum;
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, before, off);
-      if (static_cast<int>(threadIdx.x) >= off) before += y;
-    }
-    before -= sum;
-    for (int e = e0; e < e0 + per && e < a.E; ++e) {
-      before += start[e + 1];
-      start[e + 1] = before;
-    }
-  }
-}
-
-// Tile t, in bands of kBand row tiles, inside a band column by column, so that the tiles in flight
-// share their operands through L2.
-template <int BM, int BN>
-__device__ __forceinline__ Tile tile_at(const GemmArgs& a, const int* start, int t) {
-  const int tiles_m = start[a.E], tiles_n = (a.N + BN - 1) / BN;
-  const int per_band = kBand * tiles_n;
-  const int band = t / per_band;
-  const int in_band = t - band * per_band;
-  const int h = min(kBand, tiles_m - band * kBand);
-  const int mt = band * kBand + in_band % h;
-  int lo = 0, hi = a.E - 1;  // the last expert whose first row tile is at or before mt
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (start[mid] <= mt)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  // experts without rows share their successor's start: the search ends at the last of them, which
-  // is the one with rows
-  int r0, r1;
-  expert_range(a, lo, r0, r1);
-  Tile x;
-  x.e = lo;
-  x.m0 = r0 + (mt - start[lo]) * BM;
-  x.m1 = min(r1, x.m0 + BM);
-  x.n0 = in_band / h * BN;
-  return x;
-}
 
 // 16 bytes of output from fp32 sums.
 __device__ __forceinline__ uint4 pack16(const float* v, float) {
@@ -259,8 +165,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sh.accf[b], 1);
       ptx::mbar_init(&sh.acce[b], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
-    for (int s = 0; s < kScales; ++s) ptx::mbar_init(&sh.scf[s], 1);
-    for (int s = 0; s < 2; ++s) ptx::mbar_init(&sh.sce[s], kEpiWarps);
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&sh.scf[s], 1);
+      ptx::mbar_init(&sh.sce[s], kEpiWarps);
+    }
     ptx::mbar_init(&sh.drain, 1);
     sh.abort = 0;
     ptx::fence_barrier_init();
@@ -405,22 +313,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int f = 0; f < kFetch; ++f) fetch(f, f);
     bool ok = true;
-    for (int g0 = 0; g0 < blocks && ok; g0 += kFetch) {
+    for (int g0 = 0; g0 < blocks; g0 += kScaleHalf) {
+      const int half = (g0 / kScaleHalf) & 1;
+      if (g0 >= kScales) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[half], ((g0 / kScales) - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
 #pragma unroll
       for (int f = 0; f < kFetch; ++f) {
-        const int g = g0 + f;
-        if (g >= blocks || !ok) break;
-        if (g % kScaleHalf == 0 && g >= kScales)
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[(g / kScaleHalf) & 1], ((g / kScales) - 1) & 1, abort_flag));
-        if (!ok) break;
+        if (g0 + f >= blocks) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sh.scales[g % kScales][h][r * 32 + lane] = sa[f][r] * sw[f][h];
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.scf[g % kScales]);
-        fetch(f, g + kFetch);
+          for (int r = 0; r < 4; ++r) sh.scales[(g0 + f) % kScales][h][r * 32 + lane] = sa[f][r] * sw[f][h];
+        fetch(f, g0 + f + kFetch);
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.scf[half]);
     }
     if (!ok) fail();
   } else if (warp >= 4) {
@@ -433,8 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (warp - 4) >> 2;  // which half of the tile's columns
     const uint32_t tmem_w = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * NC);
     uint8_t* stage = stores + (warp - 4) * kStoreBytes;
+    const uint32_t acce = kPair ? ptx::mapa(&sh.acce[0], 0) : ptx::smem_u32(&sh.acce[0]);
+    const uint32_t sce = ptx::smem_u32(&sh.sce[0]);
     const uint32_t scale_at = ptx::smem_u32(&sh.scales[0][h][q * 32 + lane]);
-    bool ok = true, seen = false;  // seen: this block's barriers have been seen complete
+    bool ok = true, seen = false;  // seen: the block's accumulator has been seen filled
     int g = 0, turn = 0;
     for (int i = 0; i < own && ok; ++i) {
       float acc[NC];
@@ -442,10 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < NC; ++c) acc[c] = 0.f;
       for (int k = 0; k < args.kblocks; ++k, ++g) {
         const int b = g & 1;
+        // the warp goes on or gives up as one: a wait may run out for some of its lanes only
+        if (g % kScaleHalf == 0) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag));
+          if (!ok) break;
+        }
         if (!__all_sync(0xffffffffu, seen)) {
-          // the warp goes on or gives up as one: a wait may run out for some of its lanes only
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.scf[g % kScales], (g / kScales) & 1, abort_flag) &&
-                                           ptx::mbar_wait(&sh.accf[b], (g >> 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.accf[b], (g >> 1) & 1, abort_flag));
           if (!ok) break;
         }
         ptx::tc_fence_after();
@@ -469,16 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair)
-            ptx::mbar_arrive_cluster(ptx::mapa(&sh.acce[b], 0));
-          else
-            ptx::mbar_arrive(&sh.acce[b]);
-          if (g % kScaleHalf == kScaleHalf - 1) ptx::mbar_arrive(&sh.sce[(g / kScaleHalf) & 1]);
-        }
-        const int n = g + 1;
-        seen = n < blocks && ptx::mbar_try_wait(&sh.scf[n % kScales], (n / kScales) & 1) &&
-               ptx::mbar_try_wait(&sh.accf[n & 1], (n >> 1) & 1);
+        ptx::mbar_arrive_cluster(acce + 8 * b, lane == 0);
+        ptx::mbar_arrive_cluster(sce + 8 * ((g / kScaleHalf) & 1), lane == 0 && g % kScaleHalf == kScaleHalf - 1);
+        seen = ptx::mbar_test(&sh.accf[b ^ 1], ((g + 1) >> 1) & 1);
         add(NC / 32 - 2);
         add(NC / 32 - 1);
       }
@@ -506,30 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool kPair, typename TY>
 hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
   constexpr int kTile = kPair ? 256 : 128;
-  const int64_t kblocks = ceil_div(p.K, kFp8Block);
-  // an expert's rows may leave one partial row tile each
-  const int64_t most = (p.rows / kTile + (p.offsets != nullptr ? p.E : 1)) * ceil_div(p.N, kTile);
-  if (most * kblocks > 0x7FFFFFFF) return HQ_ERR_UNSUPPORTED;
-  const uint64_t pitch = static_cast<uint64_t>(fp8_pitch(p.K));
+  const int64_t most = most_tiles(p, kTile, kTile);
   CUtensorMap map_a, map_w, map_y;
-  if (!make_tmap_2d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a_codes, static_cast<uint64_t>(p.K),
-                    static_cast<uint64_t>(p.rows), pitch, kBK, kRows) ||
-      !make_tmap_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w_codes, static_cast<uint64_t>(p.K),
-                    static_cast<uint64_t>(p.E * p.N), pitch, kBK, kRows))
-    return HQ_ERR_CUDA;
   GemmArgs a{};
-  a.Y = p.Y;
-  a.rows = static_cast<int>(p.rows);
-  a.N = static_cast<int>(p.N);
-  a.K = static_cast<int>(p.K);
-  a.kblocks = static_cast<int>(kblocks);
-  a.nblocks = static_cast<int>(ceil_div(p.N, kFp8Block));
-  a.a_scales = p.a_scales;
-  a.w_scales = p.w_scales;
-  a.offsets = p.offsets;
-  a.E = static_cast<int>(p.E);
-  a.y_aligned = aligned(p.Y, 16) && p.N * sizeof(TY) % 16 == 0;
-  a.status = p.status;
+  const hq_status st = gemm_args(p, most, kRows, kRows, a, map_a, map_w);
+  if (st != HQ_OK) return st;
   if (!a.y_aligned)
     map_y = map_a;  // not used
   else if (!make_tmap_2d(&map_y, sizeof(TY) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y,
@@ -554,11 +442,25 @@ hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
 
 }  // namespace
 
+hq_status gemm_single(const Fp8Gemm& p, cudaStream_t s) {
+  return p.y_dtype == HQ_F32 ? run_gemm<false, float>(p, s) : run_gemm<false, __nv_bfloat16>(p, s);
+}
+hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
+  return p.y_dtype == HQ_F32 ? run_gemm<true, float>(p, s) : run_gemm<true, __nv_bfloat16>(p, s);
+}
+
+}  // namespace fp8
+
 hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s) {
   if (p.rows == 0) return HQ_OK;
-  if (impl == kFp8Auto) impl = p.rows / p.E >= 256 ? kFp8Pair : kFp8Single;
-  if (impl == kFp8Pair) return p.y_dtype == HQ_F32 ? run_gemm<true, float>(p, s) : run_gemm<true, __nv_bfloat16>(p, s);
-  return p.y_dtype == HQ_F32 ? run_gemm<false, float>(p, s) : run_gemm<false, __nv_bfloat16>(p, s);
+  const int64_t each = p.rows / p.E;  // rows of an expert, on average
+  if (impl == kFp8Auto) impl = each >= 256 ? kFp8Pair : each > 64 ? kFp8Single : each > 16 ? kFp8Few64 : kFp8Few16;
+  switch (impl) {
+    case kFp8Pair: return fp8::gemm_pair(p, s);
+    case kFp8Single: return fp8::gemm_single(p, s);
+    case kFp8Few64: return fp8::gemm_few(p, 64, s);
+    default: return fp8::gemm_few(p, 16, s);
+  }
 }
 
 }  // namespace hq

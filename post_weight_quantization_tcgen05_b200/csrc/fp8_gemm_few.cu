@@ -1,0 +1,355 @@
+// The e4m3 product for few rows (a serving step): bound by reading the weights.  The mathematics and
+// the scaling after every block of 128 columns are those of fp8_gemm.cu, with the operands exchanged:
+// 128 rows of W are the MMA's 128 rows, BT rows of A (16 or 64) its columns.  A block's accumulator is
+// then BT columns of tensor memory, so 256 of them hold 16 or 4 accumulators and the hand-over to the
+// epilogue, several hundred cycles, never holds up the loads; a stage takes 16 KB of W and 2 or 8 KB
+// of A, and two CTAs on an SM keep 10 stages on their way.
+//
+// Where there are fewer tiles than CTAs the GPU holds, a cluster of up to 8 CTAs shares a tile, each
+// taking a part of the K blocks.  At the end each leaves its sums in shared memory, and every CTA adds
+// up the parts of some of the tile's rows of A, in the order of the CTAs, and stores them: no workspace,
+// no second launch, the same result every time.
+//
+// Per CTA: warp 0 loads, warp 1 issues the MMAs, warp 2 leaves the products of the scales in shared
+// memory, warps 4-7 (one TMEM lane quadrant each) scale and add: a thread holds one row of W, that is a
+// column of Y, for the BT rows of A.  Neighbouring lanes store neighbouring columns.
+//
+// Every wait is bounded, as in fp8_gemm.cu.
+#include <algorithm>
+
+#include "fp8_gemm.cuh"
+
+namespace hq {
+namespace fp8 {
+namespace {
+
+constexpr int kRows = 128;  // rows of W of a tile
+constexpr int kEpiWarps = 4;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kCtasPerSM = 2;
+constexpr int kTmemCols = 256;  // of the SM's 512
+constexpr int kMaxSplit = 8;
+// blocks whose scales are kept, handed over and given back by halves; loads run kFetch blocks ahead
+constexpr int kScales = 8, kScaleHalf = kScales / 2;
+constexpr int kFetch = kScaleHalf;
+constexpr int kPlaces = 16;
+static_assert(kPlaces > kScales + kFetch, "a tile's place is overwritten after the epilogue read it");
+
+template <int BT>
+struct Shared {
+  float scales[kScales][BT];
+  Tile places[kPlaces];
+  uint64_t full[8];
+  uint64_t empty[8];
+  uint64_t accf[kTmemCols / BT];
+  uint64_t acce[kTmemCols / BT];
+  uint64_t scf[2], sce[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int start[kMaxExperts + 1];
+};
+
+template <int BT>
+struct Few {
+  static constexpr int kStageBytes = kRows * kBK + BT * kBK;
+  static constexpr int kStages = BT == 16 ? 5 : 4;
+  static constexpr int kAccs = kTmemCols / BT;
+  static constexpr int kSmem = kStages * kStageBytes + 1024 /*align*/ + static_cast<int>(sizeof(Shared<BT>));
+  static_assert(kStages <= 8 && kSmem <= 232448 / kCtasPerSM - 1024, "two CTAs on an SM");
+  static_assert(kRows * BT * 4 <= kStages * kStageBytes, "a tile's sums fit into the stages");
+};
+
+// grid: CTAs in clusters of `split`; cluster c takes tiles c, c + clusters, ...
+template <int BT, typename TY>
+__global__ void __launch_bounds__(kThreads, kCtasPerSM)
+    fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW,
+                        GemmArgs args, int split) {
+  constexpr int kStages = Few<BT>::kStages, kStageBytes = Few<BT>::kStageBytes, kAccs = Few<BT>::kAccs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared<BT>& sh = *reinterpret_cast<Shared<BT>*>(smem + kStages * kStageBytes);
+  volatile int* abort_flag = &sh.abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sh.full[s], 1);
+      ptx::mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < kAccs; ++b) {
+      ptx::mbar_init(&sh.accf[b], 1);
+      ptx::mbar_init(&sh.acce[b], kEpiWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&sh.scf[s], 1);
+      ptx::mbar_init(&sh.sce[s], kEpiWarps);
+    }
+    ptx::mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sh.tmem, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  expert_tiles<BT>(args, sh.start);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int tiles = sh.start[args.E] * ((args.N + kRows - 1) / kRows);
+  const int first = blockIdx.x / split, step = gridDim.x / split;
+  const int own = tiles > first ? (tiles - 1 - first) / step + 1 : 0;
+  // this CTA's part of the K blocks, the same for every tile
+  const int k0 = static_cast<int>(static_cast<int64_t>(rank) * args.kblocks / split);
+  const int kn = static_cast<int>(static_cast<int64_t>(rank + 1) * args.kblocks / split) - k0;
+  const int blocks = own * kn;  // they follow one another across tiles
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    record_status(args.status, HQ_ERR_TIMEOUT);
+  };
+
+  bool ok = true;
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ TMA producer
+    ptx::prefetch_tensormap(&mapA);
+    ptx::prefetch_tensormap(&mapW);
+    int g = 0;
+    for (int i = 0; i < own && ok; ++i) {
+      const Tile x = tile_at<BT, kRows>(args, sh.start, first + i * step);
+      (void)HQ_IN_BOUNDS(x.m0 < args.rows && x.n0 < args.N);
+      for (int k = 0; k < kn; ++k, ++g) {
+        const int s = g % kStages;
+        if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sw = smem + s * kStageBytes;
+        ptx::mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
+        ptx::tma_load_2d(sw, &mapW, (k0 + k) * kBK, x.e * args.N + x.n0, &sh.full[s]);
+        ptx::tma_load_2d(sw + kRows * kBK, &mapA, (k0 + k) * kBK, x.m0, &sh.full[s]);
+      }
+    }
+    if (!ok) {
+      fail();
+      // let the copies already issued land before shared memory goes away
+      for (int k = g > kStages ? g - kStages : 0; k < g; ++k)
+        ptx::mbar_wait(&sh.full[k % kStages], (k / kStages) & 1, nullptr);
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kRows, BT, false, false);
+    for (int g = 0; g < blocks; ++g) {
+      const int s = g % kStages, b = g % kAccs;
+      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag) ||
+          (g >= kAccs && !ptx::mbar_wait(&sh.acce[b], ((g / kAccs) - 1) & 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t dacc = tmem + static_cast<uint32_t>(b * BT);
+      const uint32_t sw = ptx::smem_u32(smem + s * kStageBytes);
+      const uint32_t sa = sw + kRows * kBK;
+#pragma unroll
+      for (int kk = 0; kk < kBK / 32; ++kk)
+        // K-major rows of 128 bytes, 8-row groups 1 KB apart (SBO); an MMA takes 32 bytes of each row
+        ptx::mma_f8(dacc, ptx::sdesc_sw128(sw + kk * 32, 16, 1024), ptx::sdesc_sw128(sa + kk * 32, 16, 1024), kIdesc,
+                    kk > 0 ? 1u : 0u);
+      ptx::mma_commit(&sh.accf[b]);
+      ptx::mma_commit(&sh.empty[s]);
+    }
+    if (!ok) {
+      fail();
+      ptx::mma_commit(&sh.drain);
+      ptx::mbar_wait(&sh.drain, 0, nullptr);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales
+    constexpr int kPer = (BT + 31) / 32;  // rows of A a lane fetches
+    float sa[kFetch][kPer], sw[kFetch];
+    Tile x{};
+    int k = kn, i = -1;  // the block to fetch: the first of the tile after tile i
+    auto fetch = [&](int f, int g) {
+      if (g >= blocks) return;
+      if (k == kn) {
+        k = 0;
+        ++i;
+        x = tile_at<BT, kRows>(args, sh.start, first + i * step);
+        // its place is read by the epilogue after its first block's scales are announced, later
+        if (lane == 0) sh.places[i % kPlaces] = x;
+      }
+      const float* col = args.a_scales + static_cast<int64_t>(k0 + k) * args.rows;
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+        const int row = x.m0 + r * 32 + lane;
+        sa[f][r] = row < x.m1 ? __ldg(col + row) : 0.f;
+      }
+      sw[f] = __ldg(args.w_scales + (static_cast<int64_t>(x.e) * args.nblocks + x.n0 / kFp8Block) * args.kblocks + k0 + k);
+      ++k;
+    };
+#pragma unroll
+    for (int f = 0; f < kFetch; ++f) fetch(f, f);
+    for (int g0 = 0; g0 < blocks; g0 += kScaleHalf) {
+      const int half = (g0 / kScaleHalf) & 1;
+      if (g0 >= kScales) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[half], ((g0 / kScales) - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int f = 0; f < kFetch; ++f) {
+        if (g0 + f >= blocks) break;
+#pragma unroll
+        for (int r = 0; r < kPer; ++r)
+          if (r * 32 + lane < BT) sh.scales[(g0 + f) % kScales][r * 32 + lane] = sa[f][r] * sw[f];
+        fetch(f, g0 + f + kFetch);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.scf[half]);
+    }
+    if (!ok) fail();
+  }
+
+  if (warp < 4) {
+    if (split > 1) {
+      // the other warps' share of the clusters' two meetings below
+      __syncwarp();
+      ptx::cluster_sync();
+      ptx::cluster_sync();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    const uint32_t tmem_w = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int n = q * 32 + lane;  // this thread's row of the tile's 128 of W
+    int g = 0;
+    for (int i = 0; i < own && ok; ++i) {
+      float acc[BT];
+#pragma unroll
+      for (int c = 0; c < BT; ++c) acc[c] = 0.f;
+      for (int k = 0; k < kn; ++k, ++g) {
+        const int b = g % kAccs;
+        // the warp goes on or gives up as one: a wait may run out for some of its lanes only
+        ok = __all_sync(0xffffffffu,
+                        (g % kScaleHalf != 0 ||
+                         ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag)) &&
+                            ptx::mbar_wait(&sh.accf[b], (g / kAccs) & 1, abort_flag));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const float4* scale = reinterpret_cast<const float4*>(sh.scales[g % kScales]);
+        const uint32_t from = tmem_w + static_cast<uint32_t>(b * BT);
+#pragma unroll
+        for (int c = 0; c < BT; c += 16) {
+          uint32_t r[16];
+          ptx::tmem_ld16_nowait(from + c, r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 sc = scale[(c + j) / 4];
+            acc[c + j] = fmaf(sc.x, __uint_as_float(r[j]), acc[c + j]);
+            acc[c + j + 1] = fmaf(sc.y, __uint_as_float(r[j + 1]), acc[c + j + 1]);
+            acc[c + j + 2] = fmaf(sc.z, __uint_as_float(r[j + 2]), acc[c + j + 2]);
+            acc[c + j + 3] = fmaf(sc.w, __uint_as_float(r[j + 3]), acc[c + j + 3]);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        ptx::mbar_arrive_cluster(ptx::smem_u32(&sh.acce[b]), lane == 0);
+        if (g % kScaleHalf == kScaleHalf - 1)
+          ptx::mbar_arrive_cluster(ptx::smem_u32(&sh.sce[(g / kScaleHalf) & 1]), lane == 0);
+      }
+      if (!ok) break;
+      const Tile x = sh.places[i % kPlaces];
+      const int col = x.n0 + n, left = x.m1 - x.m0;
+      if (split == 1) {
+        TY* y = static_cast<TY*>(args.Y) + static_cast<int64_t>(x.m0) * args.N + col;
+        if (col < args.N && HQ_IN_BOUNDS(x.m0 >= 0 && x.m1 <= args.rows)) {
+#pragma unroll
+          for (int c = 0; c < BT; ++c)
+            if (c < left) y[static_cast<int64_t>(c) * args.N] = static_cast<TY>(acc[c]);
+        }
+      } else {
+        // one tile per cluster: its blocks' operands have been used, the stages are free
+        float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int c = 0; c < BT; ++c) part[c * kRows + n] = acc[c];
+      }
+    }
+    if (!ok) fail();
+    if (split > 1) {
+      ptx::cluster_sync();  // every part is in its CTA's shared memory
+      if (ok && own > 0) {
+        const Tile x = sh.places[0];
+        const int col = x.n0 + n, left = x.m1 - x.m0;
+        const float* part = reinterpret_cast<const float*>(smem);
+        if (col < args.N && HQ_IN_BOUNDS(x.m0 >= 0 && x.m1 <= args.rows)) {
+          TY* y = static_cast<TY*>(args.Y) + static_cast<int64_t>(x.m0) * args.N + col;
+          for (int c = rank; c < left; c += split) {
+            float v[kMaxSplit];
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+              v[r] = r < split ? ptx::ld_cluster_f32(ptx::mapa(part + c * kRows + n, r)) : 0.f;
+            float sum = v[0];
+#pragma unroll
+            for (int r = 1; r < kMaxSplit; ++r)
+              if (r < split) sum += v[r];
+            y[static_cast<int64_t>(c) * args.N] = static_cast<TY>(sum);
+          }
+        }
+      }
+      ptx::cluster_sync();  // no CTA leaves while another reads its part
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int BT, typename TY>
+hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
+  const int64_t most = most_tiles(p, BT, kRows);
+  CUtensorMap map_a, map_w;
+  GemmArgs a{};
+  const hq_status st = gemm_args(p, most, BT, kRows, a, map_a, map_w);
+  if (st != HQ_OK) return st;
+  constexpr int kSmem = Few<BT>::kSmem;
+  HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_few_kernel<BT, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  constexpr int kSlots = kSMs * kCtasPerSM;
+  // a cluster per tile where the tiles are known (one weight) and leave CTAs idle
+  int split = 1;
+  if (p.offsets == nullptr && most * 2 <= kSlots) {
+    const int64_t tiles = ceil_div(p.rows, BT) * ceil_div(p.N, kRows);
+    split = static_cast<int>(std::min<int64_t>({kMaxSplit, kSlots / tiles, a.kblocks}));
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? ceil_div(p.rows, BT) * ceil_div(p.N, kRows) * split
+                                                     : std::min<int64_t>(most, kSlots)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  HQ_LAUNCH_CHAINED(cudaLaunchKernelEx(&cfg, fp8_gemm_few_kernel<BT, TY>, map_a, map_w, a, split));
+  return HQ_OK;
+}
+
+}  // namespace
+
+hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {
+  if (p.y_dtype == HQ_F32) return tile_rows == 16 ? run_few<16, float>(p, s) : run_few<64, float>(p, s);
+  return tile_rows == 16 ? run_few<16, __nv_bfloat16>(p, s) : run_few<64, __nv_bfloat16>(p, s);
+}
+
+}  // namespace fp8
+}  // namespace hq

@@ -215,7 +215,7 @@ struct Fp8Gemm {
   int y_dtype;
   int* status;
 };
-enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2 };
+enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2, kFp8Few16 = 3, kFp8Few64 = 4 };
 hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s);
 
 // experts.cu: R = T top choices; see there

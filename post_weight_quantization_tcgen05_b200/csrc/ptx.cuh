@@ -48,6 +48,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same, without waiting at all.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for the phase with the given parity to complete.  Gives up (returns false) after
 // `limit` cycles (kWaitLimitCycles unless stated), or as soon as *abort becomes non-zero.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -56,6 +69,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   const long long start = clock64();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
+    if (abort != nullptr && *abort) return false;
+    if (clock64() - start > limit) return false;
+  }
+}
+
+// The same by polling without a pause, for waits on the critical path: a suspended try_wait returns some
+// hundred cycles after the phase is complete.
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          long long limit = kWaitLimitCycles) {
+  const long long start = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test(bar, parity)) return true;
     if (abort != nullptr && *abort) return false;
     if (clock64() - start > limit) return false;
   }
@@ -176,11 +203,23 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on a barrier given by its address in the cluster's window (mapa).  It orders tensor-memory
-// reads only (with the tcgen05 fences around it), so it carries no cluster-wide release: that would
-// wait for every earlier global store of the warp.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrives, if `go`, on a barrier given by its address in the cluster's window (mapa; a CTA's own
+// shared-memory address lies there too).  It orders tensor-memory reads only (with the tcgen05 fences
+// around it), so it carries no cluster-wide release: that would wait for every earlier global store of
+// the warp.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, bool go) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}\n" ::"r"(bar),
+      "r"(go ? 1 : 0)
+      : "memory");
+}
+// fp32 from the cluster's window (mapa).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 // A load into this CTA's shared memory that signals a barrier of the pair (address from mapa).
 __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y,

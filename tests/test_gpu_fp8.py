@@ -332,11 +332,11 @@ def test_linear_on_a_side_stream_and_in_a_graph(hq, cuda_device, M, N, K):
 
 # ------------------------------------------------------------------ the kernels one by one
 
-IMPLS = {"single": 1, "pair": 2}
+IMPLS = {"single": 1, "pair": 2, "few16": 3, "few64": 4}
 
 
 @pytest.mark.parametrize("impl", list(IMPLS))
-@pytest.mark.parametrize("M,N,K", SHAPES + [(2900, 3400, 400), (512, 17408, 256)])
+@pytest.mark.parametrize("M,N,K", SHAPES + [(2900, 3400, 400), (512, 17408, 256), (16, 5120, 5120), (5, 17408, 640), (64, 4000, 1536)])
 def test_every_kernel_on_one_weight(hq, cuda_device, M, N, K, impl):
     a, sa = small_integers(1, M, K, 1)
     w, sw = small_integers(2, N, K, 128)
