@@ -346,8 +346,9 @@ hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t 
  * the inner sums on the tensor cores, scaled and added over the blocks in fp32, rounded once to
  * y_dtype (HQ_BF16 or HQ_F32).  Y [rows, N], row-major.
  * hq_fp8_gemm: one weight for all M rows.  M >= 0 (M == 0 is a no-op).
- * hq_fp8_linear: the same from activations X [M, K] in x_dtype, quantised into the workspace on the
- *   way: hq_fp8_quantize_rows followed by hq_fp8_gemm, with the same result.  workspace: device,
+ * hq_fp8_linear: the same from activations X [M, K] in x_dtype, quantised on the way (into the
+ *   workspace, or, for few rows, by the product's own kernel): the result of hq_fp8_quantize_rows followed by
+ *   hq_fp8_gemm, bit for bit.  workspace: device,
  *   256-byte aligned, at least hq_fp8_linear_workspace_bytes(M, K) bytes (HQ_ERR_WORKSPACE), not
  *   shared with a call that may run at the same time (another stream, or another captured graph);
  *   NULL is accepted where that size is 0.

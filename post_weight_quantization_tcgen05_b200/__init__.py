@@ -144,7 +144,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object (3 us less a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -463,11 +464,11 @@ _FP8 = (torch.float8_e4m3fn, torch.uint8)
 
 def _ptrs(*tensors):
     """The pointers of contiguous tensors (or None) that all live on the current device."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
     ptrs = []
     for t in tensors:
         ptrs.append(_ptr(t))
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"expected tensors on the current device (cuda:{dev}), got {t.device}")
     return ptrs
 
@@ -475,7 +476,7 @@ def _ptrs(*tensors):
 def _want(t, name: str, dtype, shape) -> None:
     if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
 
 

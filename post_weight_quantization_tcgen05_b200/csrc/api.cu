@@ -513,7 +513,7 @@ hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t 
 hq_status hq_fp8_gemm(const uint8_t* a_codes, const float* a_scales, int64_t M, const uint8_t* w_codes,
                       const float* w_scales, int64_t N, int64_t K, void* Y, int y_dtype, int* dev_status,
                       hq_stream_t stream) {
-  const Fp8Gemm g{a_codes, a_scales, M, nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status};
+  const Fp8Gemm g{a_codes, a_scales, M, nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status, nullptr, 0, false};
   const hq_status st = check_fp8_gemm(g);
   if (st != HQ_OK || M == 0) return st;
   return launch_fp8_gemm(g, kFp8Auto, static_cast<cudaStream_t>(stream));
@@ -531,22 +531,20 @@ hq_status hq_fp8_linear(const void* X, int x_dtype, int64_t M, const uint8_t* w_
   if (st != HQ_OK) return st;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   const Fp8Gemm g{codes, reinterpret_cast<const float*>(codes + (M > 0 ? fp8_linear_scales_offset(M, K) : 0)), M,
-                  nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status};
+                  nullptr, w_codes, w_scales, 1, N, K, Y, y_dtype, dev_status, X, x_dtype, false};
   if (M > 0 && (X == nullptr || !dtype_aligned(X, x_dtype))) return HQ_ERR_INVALID;
   if (M > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < fp8_linear_workspace(M, K)))
     return HQ_ERR_WORKSPACE;
   st = check_fp8_gemm(g);
   if (st != HQ_OK || M == 0) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = launch_fp8_rows(X, x_dtype, M, K, codes, const_cast<float*>(g.a_scales), s);
-  if (st != HQ_OK) return st;
-  return launch_fp8_gemm(g, kFp8Auto, s);
+  return launch_fp8_linear(g, codes, const_cast<float*>(g.a_scales), s);
 }
 
 hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
                              const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K, void* Y,
                              int y_dtype, int* dev_status, hq_stream_t stream) {
-  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status};
+  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status, nullptr, 0, false};
   const hq_status st = check_fp8_gemm(g);
   if (st != HQ_OK || rows == 0) return st;
   if (offsets == nullptr || !aligned(offsets, 4)) return HQ_ERR_INVALID;
@@ -556,7 +554,7 @@ hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int6
 hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
                                  const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K,
                                  void* Y, int y_dtype, int* dev_status, int impl, hq_stream_t stream) {
-  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status};
+  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status, nullptr, 0, false};
   const hq_status st = check_fp8_gemm(g);
   if (st != HQ_OK || rows == 0) return st;
   if (impl < kFp8Auto || impl > kFp8Few64 || (offsets == nullptr && E != 1)) return HQ_ERR_INVALID;

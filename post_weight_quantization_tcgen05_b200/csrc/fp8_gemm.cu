@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ TMA producer
     ptx::prefetch_tensormap(&mapA);
     ptx::prefetch_tensormap(&mapW);
+    pdl_wait();
     int g = 0;  // stages issued by this CTA
     bool ok = true;
     for (int i = 0; i < own && ok; ++i) {
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // ------------------------------------------------------------ scales
     // A lane fetches the scales of 4 rows, kFetch blocks ahead of the block it writes.
+    pdl_wait();
     float sa[kFetch][4], sw[kFetch][2];
     Tile x{};
     int k = args.kblocks, i = -1;  // the block to fetch: the first of the tile after tile i
@@ -425,18 +427,9 @@ hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
     return HQ_ERR_CUDA;
   HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<kPair, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   const int slots = kPair ? kSMs / 2 : kSMs;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((most < slots ? most : slots) * (kPair ? 2 : 1)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kPair ? 2 : 1;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 1 : 0;
-  HQ_LAUNCH_CHAINED(cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<kPair, TY>, map_a, map_w, map_y, a));
+  const unsigned grid = static_cast<unsigned>((most < slots ? most : slots) * (kPair ? 2 : 1));
+  HQ_LAUNCH_CHAINED(launch_product(p, fp8_gemm_kernel<kPair, TY>, grid, kThreads, kSmem, kPair ? 2 : 1, s, map_a, map_w,
+                                   map_y, a));
   return HQ_OK;
 }
 
@@ -451,16 +444,37 @@ hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
 
 }  // namespace fp8
 
+namespace {
+
+int pick_impl(const Fp8Gemm& p) {
+  const int64_t each = p.rows / p.E;  // rows of an expert, on average
+  return each >= 256 ? kFp8Pair : each > 64 ? kFp8Single : each > 32 ? kFp8Few64 : each > 16 ? kFp8Few32 : kFp8Few16;
+}
+
+}  // namespace
+
 hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s) {
   if (p.rows == 0) return HQ_OK;
-  const int64_t each = p.rows / p.E;  // rows of an expert, on average
-  if (impl == kFp8Auto) impl = each >= 256 ? kFp8Pair : each > 64 ? kFp8Single : each > 16 ? kFp8Few64 : kFp8Few16;
-  switch (impl) {
+  switch (impl == kFp8Auto ? pick_impl(p) : impl) {
     case kFp8Pair: return fp8::gemm_pair(p, s);
     case kFp8Single: return fp8::gemm_single(p, s);
     case kFp8Few64: return fp8::gemm_few(p, 64, s);
+    case kFp8Few32: return fp8::gemm_few(p, 32, s);
     default: return fp8::gemm_few(p, 16, s);
   }
+}
+
+// Few rows are quantised by the CTAs that multiply them, each the blocks that it needs: one launch.
+// More are quantised once, by a kernel of their own.
+hq_status launch_fp8_linear(Fp8Gemm p, uint8_t* codes, float* scales, cudaStream_t s) {
+  if (p.rows == 0) return HQ_OK;
+  const int impl = pick_impl(p);
+  if (impl == kFp8Few16 && fp8::few_quantises(p)) return fp8::gemm_few(p, 16, s);
+  const hq_status st = launch_fp8_rows(p.X, p.x_dtype, p.rows, p.K, codes, scales, s);
+  if (st != HQ_OK) return st;
+  p.X = nullptr;
+  p.chained = true;
+  return launch_fp8_gemm(p, impl, s);
 }
 
 }  // namespace hq

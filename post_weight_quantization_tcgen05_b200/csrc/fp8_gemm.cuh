@@ -47,6 +47,13 @@ __device__ __forceinline__ void expert_range(const GemmArgs& a, int e, int& r0, 
 // All threads: fills start[0 .. E] with tiles of BM rows; valid after the next barrier.
 template <int BM>
 __device__ __forceinline__ void expert_tiles(const GemmArgs& a, int* start) {
+  if (a.offsets == nullptr) {  // one matrix for all rows
+    if (threadIdx.x == 0) {
+      start[0] = 0;
+      start[1] = (a.rows + BM - 1) / BM;
+    }
+    return;
+  }
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     int r0, r1;
     expert_range(a, e, r0, r1);
@@ -132,7 +139,36 @@ inline hq_status gemm_args(const Fp8Gemm& p, int64_t tiles, uint32_t box_a, uint
   return HQ_OK;
 }
 
-hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s);  // fp8_gemm_few.cu: tiles of 16 or 64 rows
+// Launches a product's kernel: `cluster` CTAs to a cluster, and, after the kernel that quantises its
+// rows, as its dependent (the kernel calls pdl_wait before it touches codes or scales of A).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_product(const Fp8Gemm& p, void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                                  unsigned cluster, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (p.chained) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// fp8_gemm_few.cu: for few rows, in tiles of 16, 32 or 64.  With p.X (few_quantises(p), tiles of 16) the
+// rows are quantised by the kernel itself.
+bool few_quantises(const Fp8Gemm& p);
+hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s);
 
 }  // namespace fp8
 }  // namespace hq

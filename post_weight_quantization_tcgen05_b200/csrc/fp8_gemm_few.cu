@@ -1,8 +1,8 @@
 // The e4m3 product for few rows (a serving step): bound by reading the weights.  The mathematics and
 // the scaling after every block of 128 columns are those of fp8_gemm.cu, with the operands exchanged:
-// 128 rows of W are the MMA's 128 rows, BT rows of A (16 or 64) its columns.  A block's accumulator is
-// then BT columns of tensor memory, so 256 of them hold 16 or 4 accumulators and the hand-over to the
-// epilogue, several hundred cycles, never holds up the loads; a stage takes 16 KB of W and 2 or 8 KB
+// 128 rows of W are the MMA's 128 rows, BT rows of A (16, 32 or 64) its columns.  A block's accumulator
+// is then BT columns of tensor memory, so 256 of them hold 16, 8 or 4 accumulators and the hand-over to the
+// epilogue, several hundred cycles, never holds up the loads; a stage takes 16 KB of W and 2 to 8 KB
 // of A, and two CTAs on an SM keep 10 stages on their way.
 //
 // Where there are fewer tiles than CTAs the GPU holds, a cluster of up to 8 CTAs shares a tile, each
@@ -10,12 +10,20 @@
 // up the parts of some of the tile's rows of A, in the order of the CTAs, and stores them: no workspace,
 // no second launch, the same result every time.
 //
+// Of hq_fp8_linear's activations, one or a few rows are quantised here: the warps of a CTA turn the
+// blocks of its part of K into codes in shared memory while the first weights are on their way.  Every
+// tile's CTAs repeat that, but it reads little and saves a launch, which costs the host as long as the
+// kernel takes.  More rows are quantised by a kernel of their own and this one launched as its
+// dependent, with the first weights loaded meanwhile: for 16 rows of 5120 11.0 us against 13.2 us.
+//
 // Per CTA: warp 0 loads, warp 1 issues the MMAs, warp 2 leaves the products of the scales in shared
 // memory, warps 4-7 (one TMEM lane quadrant each) scale and add: a thread holds one row of W, that is a
 // column of Y, for the BT rows of A.  Neighbouring lanes store neighbouring columns.
 //
 // Every wait is bounded, as in fp8_gemm.cu.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "fp8_gemm.cuh"
 
@@ -35,9 +43,11 @@ constexpr int kFetch = kScaleHalf;
 constexpr int kPlaces = 16;
 static_assert(kPlaces > kScales + kFetch, "a tile's place is overwritten after the epilogue read it");
 
-template <int BT>
+constexpr int kPanel = 20;  // blocks of A that a CTA quantises and keeps
+
+template <int BT, bool kQuantise>
 struct Shared {
-  float scales[kScales][BT];
+  float scales[kQuantise ? kPanel : kScales][BT];
   Tile places[kPlaces];
   uint64_t full[8];
   uint64_t empty[8];
@@ -50,45 +60,58 @@ struct Shared {
   int start[kMaxExperts + 1];
 };
 
-template <int BT>
+template <int BT, bool kQuantise>
 struct Few {
-  static constexpr int kStageBytes = kRows * kBK + BT * kBK;
-  static constexpr int kStages = BT == 16 ? 5 : 4;
+  static_assert(!kQuantise || BT == 16, "16 rows are quantised");
+  static constexpr int kStageBytes = kRows * kBK + (kQuantise ? 0 : BT * kBK);
+  static constexpr int kStages = BT < 64 && !kQuantise ? 5 : 4;
+  static constexpr int kPanelBytes = kQuantise ? kPanel * BT * kBK : 0;
   static constexpr int kAccs = kTmemCols / BT;
-  static constexpr int kSmem = kStages * kStageBytes + 1024 /*align*/ + static_cast<int>(sizeof(Shared<BT>));
+  static constexpr int kSmem =
+      kStages * kStageBytes + kPanelBytes + 1024 /*align*/ + static_cast<int>(sizeof(Shared<BT, kQuantise>));
   static_assert(kStages <= 8 && kSmem <= 232448 / kCtasPerSM - 1024, "two CTAs on an SM");
   static_assert(kRows * BT * 4 <= kStages * kStageBytes, "a tile's sums fit into the stages");
 };
 
-// grid: CTAs in clusters of `split`; cluster c takes tiles c, c + clusters, ...
-template <int BT, typename TY>
+// grid: CTAs in clusters of `split`; cluster c takes tiles c, c + clusters, ...  TX: uint8_t (A's codes
+// and scales are read), or the type of the activations X, which are quantised here; then BT == 16, there
+// is a tile for every cluster, and a CTA's part of K has at most kPanel blocks.
+template <int BT, typename TY, typename TX>
 __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW,
-                        GemmArgs args, int split) {
-  constexpr int kStages = Few<BT>::kStages, kStageBytes = Few<BT>::kStageBytes, kAccs = Few<BT>::kAccs;
+                        GemmArgs args, int split, const TX* __restrict__ X, bool x_vec) {
+  constexpr bool kQuantise = !std::is_same<TX, uint8_t>::value;
+  using F = Few<BT, kQuantise>;
+  constexpr int kStages = F::kStages, kStageBytes = F::kStageBytes, kAccs = F::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Shared<BT>& sh = *reinterpret_cast<Shared<BT>*>(smem + kStages * kStageBytes);
+  uint8_t* panel = smem + kStages * kStageBytes;  // A's codes, if quantised here: 2 KB a block
+  Shared<BT, kQuantise>& sh = *reinterpret_cast<Shared<BT, kQuantise>*>(panel + F::kPanelBytes);
   volatile int* abort_flag = &sh.abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&sh.full[s], 1);
-      ptx::mbar_init(&sh.empty[s], 1);
+  // barriers by the lanes of warp 0: one after the other they take longer than the rest of the set-up
+  if (warp == 0) {
+    if (lane < kStages) {
+      ptx::mbar_init(&sh.full[lane], 1);
+      ptx::mbar_init(&sh.empty[lane], 1);
     }
-    for (int b = 0; b < kAccs; ++b) {
-      ptx::mbar_init(&sh.accf[b], 1);
-      ptx::mbar_init(&sh.acce[b], kEpiWarps);
+    if (lane < kAccs) {
+      ptx::mbar_init(&sh.accf[lane], 1);
+      ptx::mbar_init(&sh.acce[lane], kEpiWarps);
     }
-    for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(&sh.scf[s], 1);
-      ptx::mbar_init(&sh.sce[s], kEpiWarps);
+    if (lane < 2) {
+      ptx::mbar_init(&sh.scf[lane], 1);
+      ptx::mbar_init(&sh.sce[lane], kEpiWarps);
     }
-    ptx::mbar_init(&sh.drain, 1);
-    sh.abort = 0;
+    if (lane == 0) {
+      ptx::mbar_init(&sh.drain, 1);
+      sh.abort = 0;
+      if (!kQuantise) ptx::prefetch_tensormap(&mapA);
+      ptx::prefetch_tensormap(&mapW);
+    }
     ptx::fence_barrier_init();
   }
   if (warp == 1) {
@@ -114,24 +137,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
   };
 
   bool ok = true;
+  if constexpr (kQuantise) {
+    // ------------------------------------------------------------ quantisation of A
+    // Warp 0 starts the first weights on their way, the others take A: 8 lanes a block of 128 columns of
+    // a row, 16 columns a lane.  16-byte part p of row r is kept at place p ^ (r % 8), as a TMA load with
+    // the 128-byte swizzle would.
+    const Tile x = tile_at<BT, kRows>(args, sh.start, own > 0 ? first : 0);
+    if (warp == 0) {
+      if (lane == 0) {
+        sh.places[0] = x;
+        for (int g = 0; g < kStages && g < blocks; ++g) {
+          ptx::mbar_arrive_expect_tx(&sh.full[g], kRows * kBK);
+          ptx::tma_load_2d(smem + g * kStageBytes, &mapW, (k0 + g) * kBK, x.n0, &sh.full[g]);
+        }
+      }
+    } else {
+      const float* sw = args.w_scales + static_cast<int64_t>(x.n0 / kFp8Block) * args.kblocks + k0;
+      const int live = (x.m1 - x.m0) * blocks, c = lane & 7;  // blocks of the rows that are there
+      for (int u = (warp - 1) * 4 + (lane >> 3); u < blocks * BT; u += (kThreads - 32) / 8) {
+        const int r = u / kn, k = u - r * kn;
+        float v[16];
+        fp8_load16(X + static_cast<int64_t>(u < live ? x.m0 + r : 0) * args.K,
+                   static_cast<int64_t>(k0 + k) * kBK + c * 16, u < live ? args.K : 0, x_vec, v);
+        const float scale_w = u < live && c == 0 ? __ldg(sw + k) : 0.f;
+        float scale;
+        const uint4 codes = fp8_quantise_row16(v, scale);
+        *reinterpret_cast<uint4*>(panel + k * (BT * kBK) + r * kBK + ((c ^ (r & 7)) << 4)) = codes;
+        if (c == 0) sh.scales[k][r] = scale * scale_w;
+      }
+    }
+    ptx::fence_async_smem();  // the codes, to the tensor core
+    __syncthreads();
+  }
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
-    ptx::prefetch_tensormap(&mapA);
-    ptx::prefetch_tensormap(&mapW);
+    bool waited = false;
     int g = 0;
     for (int i = 0; i < own && ok; ++i) {
       const Tile x = tile_at<BT, kRows>(args, sh.start, first + i * step);
       (void)HQ_IN_BOUNDS(x.m0 < args.rows && x.n0 < args.N);
       for (int k = 0; k < kn; ++k, ++g) {
         const int s = g % kStages;
+        if (kQuantise && g < kStages) continue;  // on its way
         if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
         uint8_t* sw = smem + s * kStageBytes;
         ptx::mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
+        // the weights were there before the kernel that quantises A started
         ptx::tma_load_2d(sw, &mapW, (k0 + k) * kBK, x.e * args.N + x.n0, &sh.full[s]);
-        ptx::tma_load_2d(sw + kRows * kBK, &mapA, (k0 + k) * kBK, x.m0, &sh.full[s]);
+        if constexpr (!kQuantise) {
+          if (!waited && g + 1 < kStages && g + 1 < blocks) continue;
+          if (!waited) {
+            pdl_wait();
+            waited = true;
+            // A's boxes of the stages so far
+            for (int b = 0; b < g; ++b) {
+              const Tile t = tile_at<BT, kRows>(args, sh.start, first + b / kn * step);
+              ptx::tma_load_2d(smem + b * kStageBytes + kRows * kBK, &mapA, (k0 + b % kn) * kBK, t.m0, &sh.full[b]);
+            }
+          }
+          ptx::tma_load_2d(sw + kRows * kBK, &mapA, (k0 + k) * kBK, x.m0, &sh.full[s]);
+        }
       }
     }
     if (!ok) {
@@ -153,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       ptx::tc_fence_after();
       const uint32_t dacc = tmem + static_cast<uint32_t>(b * BT);
       const uint32_t sw = ptx::smem_u32(smem + s * kStageBytes);
-      const uint32_t sa = sw + kRows * kBK;
+      const uint32_t sa = kQuantise ? ptx::smem_u32(panel + g * (BT * kBK)) : sw + kRows * kBK;
 #pragma unroll
       for (int kk = 0; kk < kBK / 32; ++kk)
         // K-major rows of 128 bytes, 8-row groups 1 KB apart (SBO); an MMA takes 32 bytes of each row
@@ -167,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       ptx::mma_commit(&sh.drain);
       ptx::mbar_wait(&sh.drain, 0, nullptr);
     }
-  } else if (warp == 2) {
+  } else if (!kQuantise && warp == 2) {
     // ------------------------------------------------------------ scales
+    pdl_wait();
     constexpr int kPer = (BT + 31) / 32;  // rows of A a lane fetches
     float sa[kFetch][kPer], sw[kFetch];
     Tile x{};
@@ -218,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       // the other warps' share of the clusters' two meetings below
       __syncwarp();
       ptx::cluster_sync();
-      ptx::cluster_sync();
+      ptx::cluster_sync_relaxed();
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -234,12 +303,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
         const int b = g % kAccs;
         // the warp goes on or gives up as one: a wait may run out for some of its lanes only
         ok = __all_sync(0xffffffffu,
-                        (g % kScaleHalf != 0 ||
+                        (kQuantise || g % kScaleHalf != 0 ||
                          ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag)) &&
                             ptx::mbar_wait(&sh.accf[b], (g / kAccs) & 1, abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
-        const float4* scale = reinterpret_cast<const float4*>(sh.scales[g % kScales]);
+        const float4* scale = reinterpret_cast<const float4*>(sh.scales[kQuantise ? g : g % kScales]);
         const uint32_t from = tmem_w + static_cast<uint32_t>(b * BT);
 #pragma unroll
         for (int c = 0; c < BT; c += 16) {
@@ -258,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
         ptx::tc_fence_before();
         __syncwarp();
         ptx::mbar_arrive_cluster(ptx::smem_u32(&sh.acce[b]), lane == 0);
-        if (g % kScaleHalf == kScaleHalf - 1)
+        if (!kQuantise && g % kScaleHalf == kScaleHalf - 1)
           ptx::mbar_arrive_cluster(ptx::smem_u32(&sh.sce[(g / kScaleHalf) & 1]), lane == 0);
       }
       if (!ok) break;
@@ -300,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
           }
         }
       }
-      ptx::cluster_sync();  // no CTA leaves while another reads its part
+      ptx::cluster_sync_relaxed();  // no CTA leaves while another reads its part
     }
   }
 
@@ -312,43 +381,94 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
   }
 }
 
-template <int BT, typename TY>
+constexpr int kSlots = kSMs * kCtasPerSM;
+
+// How many clusters of `split` CTAs the current device holds at once, asked once: a cluster lies within
+// one GPC, so it depends on how many SMs each of the chip's GPCs has (40 clusters of 7 did not fit at
+// once although their 280 CTAs are fewer than 296, and 5120 x 5120 took 15.8 us instead of 9.9).
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int smem, int split) {
+  static std::atomic<int> known[kMaxSplit + 1];  // one per kernel
+  int n = known[split].load(std::memory_order_relaxed);
+  if (n != 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  if (n < 1) n = 1;
+  known[split].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int BT, typename TY, typename TX>
+struct Launch {
+  static constexpr int kSmem = Few<BT, !std::is_same<TX, uint8_t>::value>::kSmem;
+  // CTAs to a tile: as many as leave all tiles' clusters on the GPU at once, where the number of tiles is
+  // known (one weight).  The device is assumed to be like the first one asked.
+  static int split(const Fp8Gemm& p) {
+    const int64_t tiles = ceil_div(p.rows, BT) * ceil_div(p.N, kRows);
+    if (p.offsets != nullptr || tiles * 2 > kSlots) return 1;
+    for (int n = static_cast<int>(std::min<int64_t>({kMaxSplit, kSlots / tiles, ceil_div(p.K, kFp8Block)})); n > 1; --n)
+      if (tiles <= clusters_at_once(fp8_gemm_few_kernel<BT, TY, TX>, kSmem, n)) return n;
+    return 1;
+  }
+};
+
+template <int BT, typename TY, typename TX>
 hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
   const int64_t most = most_tiles(p, BT, kRows);
   CUtensorMap map_a, map_w;
   GemmArgs a{};
   const hq_status st = gemm_args(p, most, BT, kRows, a, map_a, map_w);
   if (st != HQ_OK) return st;
-  constexpr int kSmem = Few<BT>::kSmem;
-  HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_few_kernel<BT, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  constexpr int kSlots = kSMs * kCtasPerSM;
-  // a cluster per tile where the tiles are known (one weight) and leave CTAs idle
-  int split = 1;
-  if (p.offsets == nullptr && most * 2 <= kSlots) {
-    const int64_t tiles = ceil_div(p.rows, BT) * ceil_div(p.N, kRows);
-    split = static_cast<int>(std::min<int64_t>({kMaxSplit, kSlots / tiles, a.kblocks}));
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? ceil_div(p.rows, BT) * ceil_div(p.N, kRows) * split
-                                                     : std::min<int64_t>(most, kSlots)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
-  HQ_LAUNCH_CHAINED(cudaLaunchKernelEx(&cfg, fp8_gemm_few_kernel<BT, TY>, map_a, map_w, a, split));
+  constexpr int kSmem = Launch<BT, TY, TX>::kSmem;
+  const auto kernel = fp8_gemm_few_kernel<BT, TY, TX>;
+  HQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  const int split = Launch<BT, TY, TX>::split(p);
+  const int64_t clusters = split > 1 ? ceil_div(p.rows, BT) * ceil_div(p.N, kRows) : std::min<int64_t>(most, kSlots);
+  HQ_LAUNCH_CHAINED(launch_product(p, kernel, static_cast<unsigned>(clusters * split), kThreads, kSmem,
+                                   static_cast<unsigned>(split), s, map_a, map_w, a, split,
+                                   static_cast<const TX*>(p.X),
+                                   aligned(p.X, 16) && p.K * static_cast<int64_t>(sizeof(TX)) % 16 == 0));
   return HQ_OK;
+}
+
+template <typename TY>
+hq_status run_few_as(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {
+  if (tile_rows == 64) return run_few<64, TY, uint8_t>(p, s);
+  if (tile_rows == 32) return run_few<32, TY, uint8_t>(p, s);
+  if (p.X == nullptr) return run_few<16, TY, uint8_t>(p, s);
+  return p.x_dtype == HQ_F32 ? run_few<16, TY, float>(p, s) : run_few<16, TY, __nv_bfloat16>(p, s);
+}
+
+template <typename TY, typename TX>
+int panel_blocks(const Fp8Gemm& p) {
+  return static_cast<int>(ceil_div(ceil_div(p.K, kFp8Block), Launch<16, TY, TX>::split(p)));
 }
 
 }  // namespace
 
+bool few_quantises(const Fp8Gemm& p) {
+  if (p.offsets != nullptr || p.rows > 4 || ceil_div(p.N, kRows) > kSlots) return false;
+  const bool x32 = p.x_dtype == HQ_F32;
+  const int n = p.y_dtype == HQ_F32
+                    ? (x32 ? panel_blocks<float, float>(p) : panel_blocks<float, __nv_bfloat16>(p))
+                    : (x32 ? panel_blocks<__nv_bfloat16, float>(p) : panel_blocks<__nv_bfloat16, __nv_bfloat16>(p));
+  return n <= kPanel;
+}
+
 hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {
-  if (p.y_dtype == HQ_F32) return tile_rows == 16 ? run_few<16, float>(p, s) : run_few<64, float>(p, s);
-  return tile_rows == 16 ? run_few<16, __nv_bfloat16>(p, s) : run_few<64, __nv_bfloat16>(p, s);
+  return p.y_dtype == HQ_F32 ? run_few_as<float>(p, tile_rows, s) : run_few_as<__nv_bfloat16>(p, tile_rows, s);
 }
 
 }  // namespace fp8

@@ -17,6 +17,7 @@ template <typename TX>
 __global__ void __launch_bounds__(32 * kFp8RowsPerCta)
     fp8_rows_kernel(const TX* __restrict__ X, int64_t M, int64_t K, int64_t pitch, bool vec,
                     uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  pdl_launch_dependents();  // a product launched behind this kernel may set itself up meanwhile
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kFp8RowsPerCta + (threadIdx.x >> 5);
   if (row >= M) return;

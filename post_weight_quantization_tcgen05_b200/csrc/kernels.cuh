@@ -214,9 +214,16 @@ struct Fp8Gemm {
   void* Y;
   int y_dtype;
   int* status;
+  // hq_fp8_linear: the activations themselves [rows, K] (the codes and scales above are then the
+  // workspace that they are quantised into, which few rows do without), and whether the kernel before
+  // on the stream is the one that quantises them (launch_chained)
+  const void* X;
+  int x_dtype;
+  bool chained;
 };
-enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2, kFp8Few16 = 3, kFp8Few64 = 4 };
+enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2, kFp8Few16 = 3, kFp8Few32 = 4, kFp8Few64 = 5 };
 hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s);
+hq_status launch_fp8_linear(Fp8Gemm p, uint8_t* codes, float* scales, cudaStream_t s);
 
 // experts.cu: R = T top choices; see there
 constexpr int kMaxExperts = 1024;

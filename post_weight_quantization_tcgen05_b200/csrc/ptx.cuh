@@ -203,6 +203,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without ordering the global stores before it (which would wait for them).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Arrives, if `go`, on a barrier given by its address in the cluster's window (mapa; a CTA's own
 // shared-memory address lies there too).  It orders tensor-memory reads only (with the tcgen05 fences
 // around it), so it carries no cluster-wide release: that would wait for every earlier global store of
