@@ -23,7 +23,8 @@ namespace hq {
 // counts from the others: one launch.  Integer counts only, so the order is the same every time.
 constexpr int kSortWarps = 16;
 constexpr int kSortChunk = 2048;     // ids per CTA of a long list, at least
-constexpr int kSortOneChunk = 8192;  // up to here one CTA sorts alone
+constexpr int kSortOneChunk = 4096;  // up to here one CTA sorts alone
+constexpr int kSortBatch = 8;        // ids a lane loads at once
 constexpr int kSortMaxCtas = 148;
 
 struct SortSplit {
@@ -42,15 +43,25 @@ size_t expert_sort_workspace(int64_t R, int64_t E) {
   return sp.chunks == 1 ? 256 : round_up(static_cast<size_t>(sp.chunks) * E * sizeof(int), 256);
 }
 
+// ids i, i + step, ... below `end` (-1 past it), all on their way at once
+__device__ __forceinline__ void load_ids(const int* ids, int64_t i, int64_t end, int step, int (&id)[kSortBatch]) {
+#pragma unroll
+  for (int u = 0; u < kSortBatch; ++u) id[u] = i + u * step < end ? __ldg(ids + i + u * step) : -1;
+}
+
 __global__ void __launch_bounds__(32 * kSortWarps)
     expert_hist_kernel(const int* __restrict__ ids, int64_t R, int64_t chunk, int E, int* __restrict__ hist) {
   extern __shared__ int count[];
+  pdl_launch_dependents();  // expert_place_kernel counts its own ids meanwhile
   for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
   __syncthreads();
   const int64_t i0 = blockIdx.x * chunk, i1 = min(R, i0 + chunk);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
-    const unsigned e = static_cast<unsigned>(ids[i]);
-    if (e < static_cast<unsigned>(E)) atomicAdd(&count[e], 1);
+  int id[kSortBatch];
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortBatch * blockDim.x) {
+    load_ids(ids, i, i1, blockDim.x, id);
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u)
+      if (static_cast<unsigned>(id[u]) < static_cast<unsigned>(E)) atomicAdd(&count[id[u]], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[static_cast<int64_t>(blockIdx.x) * E + e] = count[e];
@@ -77,7 +88,7 @@ __device__ __forceinline__ int block_exclusive_sum(int v, int* warp_sum) {
 __global__ void __launch_bounds__(32 * kSortWarps)
     expert_place_kernel(const int* __restrict__ ids, int64_t R, int64_t chunk, int E, const int* __restrict__ hist,
                         int* __restrict__ offsets, int* __restrict__ order, int* __restrict__ position) {
-  extern __shared__ int next[];  // [warps][E]: the next row of each expert for each warp's ids
+  extern __shared__ int next[];  // [warps][E]: the next row of each expert for each warp's ids; then sums
   __shared__ int warp_sum[kSortWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t i0 = blockIdx.x * chunk, i1 = min(R, i0 + chunk);
@@ -86,11 +97,45 @@ __global__ void __launch_bounds__(32 * kSortWarps)
 
   for (int k = threadIdx.x; k < kSortWarps * E; k += blockDim.x) next[k] = 0;
   __syncthreads();
-  for (int64_t i = w0 + lane; i < w1; i += 32) {
-    const unsigned e = static_cast<unsigned>(ids[i]);
-    if (e < static_cast<unsigned>(E)) atomicAdd(&next[warp * E + e], 1);
+  int id[kSortBatch];
+  for (int64_t i = w0 + lane; i < w1; i += 32 * kSortBatch) {
+    load_ids(ids, i, w1, 32, id);
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u)
+      if (static_cast<unsigned>(id[u]) < static_cast<unsigned>(E)) atomicAdd(&next[warp * E + id[u]], 1);
   }
   __syncthreads();
+
+  // Sums over the chunks by groups of P lanes, so that an expert's counts are not read one after the
+  // other: lane r of a group takes the chunks r, r + P, ...
+  int* const sums = next + kSortWarps * E;  // [2][E]: all chunks', and those before this one
+  if (hist != nullptr) {
+    pdl_wait();
+    int P = 32;
+    while (P > 1 && P * E > static_cast<int>(blockDim.x)) P /= 2;
+    const int r = threadIdx.x % P;
+    for (int eb = 0; eb < E; eb += blockDim.x / P) {
+      const int e = eb + threadIdx.x / P;
+      int total = 0, before = 0;
+      if (e < E) {
+#pragma unroll 8
+        for (int b = r; b < static_cast<int>(gridDim.x); b += P) {
+          const int c = __ldcg(hist + static_cast<int64_t>(b) * E + e);
+          if (b < static_cast<int>(blockIdx.x)) before += c;
+          total += c;
+        }
+      }
+      for (int off = P / 2; off > 0; off /= 2) {
+        total += __shfl_xor_sync(0xffffffffu, total, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+      }
+      if (e < E && r == 0) {
+        sums[e] = total;
+        sums[E + e] = before;
+      }
+    }
+    __syncthreads();
+  }
 
   int base = 0;  // rows of the experts handled so far
   for (int eb = 0; eb < E; eb += blockDim.x) {
@@ -98,11 +143,8 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     int total = 0, before = 0;
     if (e < E) {
       if (hist != nullptr) {
-        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-          const int c = hist[static_cast<int64_t>(b) * E + e];
-          if (b < static_cast<int>(blockIdx.x)) before += c;
-          total += c;
-        }
+        total = sums[e];
+        before = sums[E + e];
       } else {
         for (int w = 0; w < kSortWarps; ++w) total += next[w * E + e];
       }
@@ -126,19 +168,24 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     __syncthreads();
   }
 
-  for (int64_t i = w0 + lane; i - lane < w1; i += 32) {
-    const unsigned e = i < w1 ? static_cast<unsigned>(ids[i]) : 0xFFFFFFFFu;
-    const bool kept = e < static_cast<unsigned>(E);
-    const unsigned same = __match_any_sync(0xffffffffu, kept ? e : 0xFFFFFFFFu);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int at = 0;
-    if (kept) at = next[warp * E + e] + rank;
-    __syncwarp();
-    if (kept && rank == __popc(same) - 1) next[warp * E + e] = at + 1;
-    __syncwarp();
-    if (i < w1 && HQ_IN_BOUNDS(!kept || (at >= 0 && at < R))) {
-      position[i] = kept ? at : -1;
-      if (kept) order[at] = static_cast<int>(i);
+  for (int64_t i0w = w0; i0w < w1; i0w += 32 * kSortBatch) {
+    load_ids(ids, i0w + lane, w1, 32, id);
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u) {
+      const int64_t i = i0w + 32 * u + lane;
+      if (i - lane >= w1) break;  // the whole warp
+      const bool kept = static_cast<unsigned>(id[u]) < static_cast<unsigned>(E);
+      const unsigned same = __match_any_sync(0xffffffffu, kept ? id[u] : -1);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      int at = 0;
+      if (kept) at = next[warp * E + id[u]] + rank;
+      __syncwarp();
+      if (kept && rank == __popc(same) - 1) next[warp * E + id[u]] = at + 1;
+      __syncwarp();
+      if (i < w1 && HQ_IN_BOUNDS(!kept || (at >= 0 && at < R))) {
+        position[i] = kept ? at : -1;
+        if (kept) order[at] = static_cast<int>(i);
+      }
     }
   }
 }
@@ -153,11 +200,16 @@ hq_status launch_expert_sort(const int* ids, int64_t R, int64_t E, int* offsets,
     expert_hist_kernel<<<sp.chunks, 32 * kSortWarps, E * sizeof(int), s>>>(ids, R, sp.chunk, e, hist);
     HQ_LAUNCH_CHECK();
   }
-  const size_t smem = static_cast<size_t>(kSortWarps) * E * sizeof(int);
+  constexpr size_t kPer = (kSortWarps + 2) * sizeof(int);
   HQ_CUDA_TRY(cudaFuncSetAttribute(expert_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(kSortWarps * kMaxExperts * sizeof(int))));
-  expert_place_kernel<<<sp.chunks, 32 * kSortWarps, smem, s>>>(ids, R, sp.chunk, e, hist, offsets, order, position);
-  HQ_LAUNCH_CHECK();
+                                   static_cast<int>(kPer * kMaxExperts)));
+  if (sp.chunks > 1) {
+    HQ_LAUNCH_CHAINED(launch_chained(expert_place_kernel, dim3(sp.chunks), dim3(32 * kSortWarps), kPer * E, s, ids, R,
+                                     sp.chunk, e, hist, offsets, order, position));
+  } else {
+    expert_place_kernel<<<1, 32 * kSortWarps, kPer * E, s>>>(ids, R, sp.chunk, e, nullptr, offsets, order, position);
+    HQ_LAUNCH_CHECK();
+  }
   return HQ_OK;
 }
 
@@ -167,48 +219,71 @@ hq_status launch_expert_sort(const int* ids, int64_t R, int64_t E, int* offsets,
 // vectors, in powers of two), and each thread one vector of 16 bytes at a time; rows that are not
 // made of aligned 16-byte vectors are walked element by element by the same code.
 template <typename T>
-struct Vec {
-  static constexpr int kN = 16 / sizeof(T);
-  __device__ static void load(const T* p, float (&v)[kN]);
-  __device__ static void store(T* p, const float (&v)[kN]);
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  using Raw = uint4;
+  __device__ __forceinline__ static Raw load(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ static void values(const Raw& a, float (&v)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ static Raw pack(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, const Raw& a) { *reinterpret_cast<uint4*>(p) = a; }
 };
 template <>
-__device__ __forceinline__ void Vec<__nv_bfloat16>::load(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+struct Vec<float> {
+  static constexpr int kN = 4;
+  using Raw = float4;
+  __device__ __forceinline__ static Raw load(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ static void values(const Raw& a, float (&v)[4]) {
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = a.z;
+    v[3] = a.w;
   }
-}
-template <>
-__device__ __forceinline__ void Vec<__nv_bfloat16>::store(__nv_bfloat16* p, const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <>
-__device__ __forceinline__ void Vec<float>::load(const float* p, float (&v)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = a.z;
-  v[3] = a.w;
-}
-template <>
-__device__ __forceinline__ void Vec<float>::store(float* p, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
+  __device__ __forceinline__ static Raw pack(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
+  __device__ __forceinline__ static void store(float* p, const Raw& a) { *reinterpret_cast<float4*>(p) = a; }
+};
 template <typename T>
 struct One {  // one element
   static constexpr int kN = 1;
-  __device__ static void load(const T* p, float (&v)[1]) { v[0] = static_cast<float>(*p); }
-  __device__ static void store(T* p, const float (&v)[1]) { *p = static_cast<T>(v[0]); }
+  using Raw = T;
+  __device__ __forceinline__ static Raw load(const T* p) { return *p; }
+  __device__ __forceinline__ static void values(const Raw& a, float (&v)[1]) { v[0] = static_cast<float>(a); }
+  __device__ __forceinline__ static Raw pack(const float (&v)[1]) { return static_cast<T>(v[0]); }
+  __device__ __forceinline__ static void store(T* p, const Raw& a) { *p = a; }
+};
+
+// Choices handled at once: their positions and weights are in registers, and their rows' loads on
+// their way together.
+constexpr int kChoices = 8;
+
+struct Choices {
+  int p[kChoices];  // -1: dropped, or none
+  float w[kChoices];
+  __device__ __forceinline__ void load(const int* position, const float* weights, int j0, int top, int64_t rows) {
+#pragma unroll
+    for (int j = 0; j < kChoices; ++j) {
+      p[j] = j0 + j < top ? __ldg(position + j0 + j) : -1;
+      if (p[j] >= rows) p[j] = -1;
+      if (p[j] < 0) p[j] = -1;
+      w[j] = weights == nullptr ? 1.f : p[j] >= 0 ? __ldg(weights + j0 + j) : 0.f;
+    }
+  }
 };
 
 constexpr int kRowThreads = 256;
@@ -232,8 +307,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const int64_t vectors = K / N;
   const int* pos = position + t * top;
   for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
-    float v[N];
-    V<T>::load(X + t * K + i * N, v);
+    const typename V<T>::Raw v = V<T>::load(X + t * K + i * N);
     for (int j = 0; j < top; ++j) {
       const int p = __ldg(pos + j);
       if (p >= 0 && p < rows) V<T>::store(out + static_cast<int64_t>(p) * K + i * N, v);
@@ -245,16 +319,18 @@ __global__ void __launch_bounds__(kRowThreads)
 // A warp takes 512 columns of one token.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    expert_dispatch_fp8_kernel(const T* __restrict__ X, int64_t tokens, int64_t K, int64_t pitch, bool vec,
+    expert_dispatch_fp8_kernel(const T* __restrict__ X, int64_t tokens, int64_t K, int64_t pitch,
                                const int* __restrict__ position, int top, int64_t rows, uint8_t* __restrict__ codes,
                                float* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (t >= tokens) return;
   const int64_t col = static_cast<int64_t>(blockIdx.y) * 512 + lane * 16;
-  float v[16];
-  fp8_load16(X + t * K, col, K, vec, v);
-  float scale;
+  Raw16<T, false> raw;
+  raw.load(X, X + tokens * K, X + t * K + col, K - col);
+  float v[16], scale;
+  raw.align();
+  raw.values(v);
   const uint4 c = fp8_quantise_row16(v, scale);
   const int* pos = position + t * top;
   for (int j = 0; j < top; ++j) {
@@ -270,7 +346,7 @@ __global__ void __launch_bounds__(256)
 
 // Y[t] = sum_j w[t, j] rows[position[t, j]] in the order of j, summed in fp32 and rounded once.
 template <typename T, template <typename> class V>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 3)
     expert_combine_kernel(const T* __restrict__ rows, int64_t nrows, int64_t K, const int* __restrict__ position,
                           const float* __restrict__ weights, int64_t tokens, int top, int tpt, T* __restrict__ Y) {
   constexpr int N = V<T>::kN;
@@ -278,78 +354,83 @@ __global__ void __launch_bounds__(kRowThreads)
   if (t >= tokens) return;
   const int64_t vectors = K / N;
   const int* pos = position + t * top;
+  const float* wt = weights != nullptr ? weights + t * top : nullptr;
+  Choices c;
+  c.load(pos, wt, 0, top, nrows);
   for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
-    for (int j = 0; j < top; ++j) {
-      const int p = __ldg(pos + j);
-      if (p < 0 || p >= nrows) continue;
-      const float w = weights != nullptr ? __ldg(weights + t * top + j) : 1.f;
-      float z[N];
-      V<T>::load(rows + static_cast<int64_t>(p) * K + i * N, z);
+    for (int j0 = 0; j0 < top; j0 += kChoices) {
+      if (top > kChoices) c.load(pos, wt, j0, top, nrows);
+      typename V<T>::Raw raw[kChoices];
 #pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] = fmaf(w, z[k], acc[k]);
+      for (int j = 0; j < kChoices; ++j)
+        if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K + i * N);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        if (c.p[j] < 0) continue;
+        float z[N];
+        V<T>::values(raw[j], z);
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] = fmaf(c.w[j], z[k], acc[k]);
+      }
     }
-    V<T>::store(Y + t * K + i * N, acc);
+    V<T>::store(Y + t * K + i * N, V<T>::pack(acc));
   }
 }
 
 // The gradient of the combine: d_rows[p] = w[t, j] dY[t] and d_weights[t, j] = <dY[t], rows[p]>,
 // p = position[t, j]; a dropped choice has d_weights 0.  Eight choices at a time, their dot products
 // in registers; a token's threads add them up in a fixed order.
-constexpr int kBackTop = 8;
 template <typename T, template <typename> class V>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 3)
     expert_combine_backward_kernel(const T* __restrict__ dY, const T* __restrict__ rows, int64_t nrows, int64_t K,
                                    const int* __restrict__ position, const float* __restrict__ weights, int64_t tokens,
                                    int top, int tpt, T* __restrict__ d_rows, float* __restrict__ d_weights) {
   constexpr int N = V<T>::kN;
-  __shared__ float part[kRowThreads / 32][kBackTop];
+  __shared__ float part[kRowThreads / 32][kChoices];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
   const bool live = t < tokens;  // all threads stay for the barriers
   const int64_t vectors = live ? K / N : 0;
-  for (int j0 = 0; j0 < top; j0 += kBackTop) {
-    const int nj = min(kBackTop, top - j0);
-    int p[kBackTop];
-    float w[kBackTop], dot[kBackTop];
-#pragma unroll
-    for (int j = 0; j < kBackTop; ++j) {
-      p[j] = live && j < nj ? __ldg(position + t * top + j0 + j) : -1;
-      if (p[j] >= nrows) p[j] = -1;
-      w[j] = p[j] >= 0 ? __ldg(weights + t * top + j0 + j) : 0.f;
-      dot[j] = 0.f;
-    }
+  for (int j0 = 0; j0 < top; j0 += kChoices) {
+    Choices c;
+    c.load(position + t * top, weights + t * top, j0, live ? top : 0, nrows);
+    float dot[kChoices] = {};
     for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
-      float g[N];
-      V<T>::load(dY + t * K + i * N, g);
+      typename V<T>::Raw raw[kChoices];
+      const typename V<T>::Raw raw_g = V<T>::load(dY + t * K + i * N);
 #pragma unroll
-      for (int j = 0; j < kBackTop; ++j) {
-        if (p[j] < 0) continue;
-        const int64_t at = static_cast<int64_t>(p[j]) * K + i * N;
+      for (int j = 0; j < kChoices; ++j)
+        if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K + i * N);
+      float g[N];
+      V<T>::values(raw_g, g);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        if (c.p[j] < 0) continue;
         float z[N], d[N];
-        V<T>::load(rows + at, z);
+        V<T>::values(raw[j], z);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           dot[j] = fmaf(g[k], z[k], dot[j]);
-          d[k] = w[j] * g[k];
+          d[k] = c.w[j] * g[k];
         }
-        V<T>::store(d_rows + at, d);
+        V<T>::store(d_rows + static_cast<int64_t>(c.p[j]) * K + i * N, V<T>::pack(d));
       }
     }
 #pragma unroll
-    for (int j = 0; j < kBackTop; ++j) {
+    for (int j = 0; j < kChoices; ++j) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], off);
     }
     if (lane == 0) {
 #pragma unroll
-      for (int j = 0; j < kBackTop; ++j) part[warp][j] = dot[j];
+      for (int j = 0; j < kChoices; ++j) part[warp][j] = dot[j];
     }
     __syncthreads();
-    if (live && threadIdx.x % tpt < nj) {
-      const int j = threadIdx.x % tpt;
+    const int j = threadIdx.x % tpt;
+    if (live && j < kChoices && j0 + j < top) {
       float sum = 0.f;
       for (int k = 0; k < tpt / 32; ++k) sum += part[warp + k][j];
       d_weights[t * top + j0 + j] = sum;
@@ -407,13 +488,11 @@ hq_status launch_expert_dispatch_fp8(const void* X, int x_dtype, int64_t tokens,
   const int64_t rows = tokens * top;
   const int n = static_cast<int>(top);
   if (x_dtype == HQ_BF16)
-    expert_dispatch_fp8_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(X), tokens, K, fp8_pitch(K), aligned(X, 16) && K % 8 == 0, position, n, rows,
-        codes, scales);
+    expert_dispatch_fp8_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(X), tokens, K, fp8_pitch(K),
+                                                    position, n, rows, codes, scales);
   else
-    expert_dispatch_fp8_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(X), tokens, K, fp8_pitch(K),
-                                                           aligned(X, 16) && K % 4 == 0, position, n, rows, codes,
-                                                           scales);
+    expert_dispatch_fp8_kernel<<<grid, 256, 0, s>>>(static_cast<const float*>(X), tokens, K, fp8_pitch(K), position, n,
+                                                    rows, codes, scales);
   HQ_LAUNCH_CHECK();
   return HQ_OK;
 }

@@ -79,7 +79,7 @@ struct Few {
 template <int BT, typename TY, typename TX>
 __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW,
-                        GemmArgs args, int split, const TX* __restrict__ X, bool x_vec) {
+                        GemmArgs args, int split, const TX* __restrict__ X) {
   constexpr bool kQuantise = !std::is_same<TX, uint8_t>::value;
   using F = Few<BT, kQuantise>;
   constexpr int kStages = F::kStages, kStageBytes = F::kStageBytes, kAccs = F::kAccs;
@@ -156,11 +156,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       const int live = (x.m1 - x.m0) * blocks, c = lane & 7;  // blocks of the rows that are there
       for (int u = (warp - 1) * 4 + (lane >> 3); u < blocks * BT; u += (kThreads - 32) / 8) {
         const int r = u / kn, k = u - r * kn;
-        float v[16];
-        fp8_load16(X + static_cast<int64_t>(u < live ? x.m0 + r : 0) * args.K,
-                   static_cast<int64_t>(k0 + k) * kBK + c * 16, u < live ? args.K : 0, x_vec, v);
+        const int64_t col = static_cast<int64_t>(k0 + k) * kBK + c * 16;
+        Raw16<TX, false> raw;
+        raw.load(X, X + static_cast<int64_t>(args.rows) * args.K,
+                 X + static_cast<int64_t>(u < live ? x.m0 + r : 0) * args.K + col, u < live ? args.K - col : 0);
         const float scale_w = u < live && c == 0 ? __ldg(sw + k) : 0.f;
-        float scale;
+        float v[16], scale;
+        raw.align();
+        raw.values(v);
         const uint4 codes = fp8_quantise_row16(v, scale);
         *reinterpret_cast<uint4*>(panel + k * (BT * kBK) + r * kBK + ((c ^ (r & 7)) << 4)) = codes;
         if (c == 0) sh.scales[k][r] = scale * scale_w;
@@ -438,8 +441,7 @@ hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
   const int64_t clusters = split > 1 ? ceil_div(p.rows, BT) * ceil_div(p.N, kRows) : std::min<int64_t>(most, kSlots);
   HQ_LAUNCH_CHAINED(launch_product(p, kernel, static_cast<unsigned>(clusters * split), kThreads, kSmem,
                                    static_cast<unsigned>(split), s, map_a, map_w, a, split,
-                                   static_cast<const TX*>(p.X),
-                                   aligned(p.X, 16) && p.K * static_cast<int64_t>(sizeof(TX)) % 16 == 0));
+                                   static_cast<const TX*>(p.X)));
   return HQ_OK;
 }
 

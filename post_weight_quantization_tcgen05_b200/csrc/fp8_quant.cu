@@ -8,49 +8,63 @@
 
 namespace hq {
 
-// Rows: a warp takes 512 columns (four blocks) of one row, the 8 warps of a CTA 8 consecutive
-// rows, so that the scales, stored [block][row], leave in 32-byte pieces.
-constexpr int kFp8RowsPerCta = 8;
+// Rows: a warp takes 512 columns (four blocks) of two rows, both on their way at once; the 8 warps of a
+// CTA 16 consecutive rows, so that the scales, stored [block][row], leave in 32-byte pieces.
+constexpr int kFp8RowsPerCta = 16;
 constexpr int kFp8ColsPerWarp = 512;
 
-template <typename TX>
-__global__ void __launch_bounds__(32 * kFp8RowsPerCta)
-    fp8_rows_kernel(const TX* __restrict__ X, int64_t M, int64_t K, int64_t pitch, bool vec,
-                    uint8_t* __restrict__ codes, float* __restrict__ scales) {
+template <bool kAligned, typename TX>
+__global__ void __launch_bounds__(256, kAligned && sizeof(TX) == 2 ? 6 : 4)
+    fp8_rows_kernel(const TX* __restrict__ X, int64_t M, int64_t K, int64_t pitch, uint8_t* __restrict__ codes,
+                    float* __restrict__ scales) {
   pdl_launch_dependents();  // a product launched behind this kernel may set itself up meanwhile
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kFp8RowsPerCta + (threadIdx.x >> 5);
-  if (row >= M) return;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kFp8RowsPerCta + (threadIdx.x >> 5);
   const int64_t col = static_cast<int64_t>(blockIdx.y) * kFp8ColsPerWarp + lane * 16;
-  float v[16];
-  fp8_load16(X + row * K, col, K, vec, v);
-  float scale;
-  const uint4 c = fp8_quantise_row16(v, scale);
-  if (col < pitch && HQ_IN_BOUNDS(col + 16 <= pitch)) *reinterpret_cast<uint4*>(codes + row * pitch + col) = c;
-  if ((lane & 7) == 0 && col < K) scales[(col / kFp8Block) * M + row] = scale;
+  Raw16<TX, kAligned> raw[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (row0 + 8 * i < M) raw[i].load(X, X + M * K, X + (row0 + 8 * i) * K + col, K - col);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = row0 + 8 * i;
+    if (row >= M) break;  // the whole warp
+    float v[16], scale;
+    raw[i].align();
+    raw[i].values(v);
+    const uint4 c = fp8_quantise_row16(v, scale);
+    if (col < pitch && HQ_IN_BOUNDS(col + 16 <= pitch)) *reinterpret_cast<uint4*>(codes + row * pitch + col) = c;
+    if ((lane & 7) == 0 && col < K) scales[(col / kFp8Block) * M + row] = scale;
+  }
 }
 
-// Weights: a CTA takes one 128 x 128 block; a thread holds 16 columns of 4 rows 32 apart.
-template <typename TX>
-__global__ void __launch_bounds__(256)
-    fp8_blocks_kernel(const TX* __restrict__ W, int64_t N, int64_t K, int64_t pitch, bool vec,
-                      uint8_t* __restrict__ codes, float* __restrict__ scales) {
+// Weights: a CTA takes one 128 x 128 block; a thread holds 16 columns of 4 rows 32 apart, kept as they
+// lie in memory (half the registers of bf16, twice the CTAs on an SM).
+template <bool kAligned, typename TX>
+__global__ void __launch_bounds__(256, sizeof(TX) == 2 ? 3 : 2)
+    fp8_blocks_kernel(const TX* __restrict__ W, int64_t N, int64_t K, int64_t pitch, uint8_t* __restrict__ codes,
+                      float* __restrict__ scales) {
   __shared__ uint32_t warp_max[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t kb = blockIdx.x, nb = blockIdx.y, e = blockIdx.z;
   const int64_t col = kb * kFp8Block + (threadIdx.x & 7) * 16;
   const int64_t row0 = nb * kFp8Block + (threadIdx.x >> 3);
-  float v[4][16];
-  uint32_t m = 0;
+  const TX* const end = W + gridDim.z * N * K;
+  Raw16<TX, kAligned> raw[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int64_t row = row0 + 32 * p;
-    fp8_load16(W + (e * N + (row < N ? row : 0)) * K, col, row < N ? K : 0, vec, v[p]);
+    raw[p].load(W, end, W + (e * N + (row < N ? row : 0)) * K + col, row < N ? K - col : 0);
   }
+  uint32_t m = 0;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) m = max(m, fp8_amax16(v[p]));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  for (int p = 0; p < 4; ++p) {
+    float v[16];
+    raw[p].align();
+    raw[p].values(v);
+    m = max(m, fp8_amax16(v));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) warp_max[warp] = m;
   __syncthreads();
 #pragma unroll
@@ -60,22 +74,19 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int64_t row = row0 + 32 * p;
+    float v[16];
+    raw[p].values(v);
     if (row < N && col < pitch && HQ_IN_BOUNDS(col + 16 <= pitch))
-      *reinterpret_cast<uint4*>(codes + (e * N + row) * pitch + col) = fp8_codes16(v[p], factor);
+      *reinterpret_cast<uint4*>(codes + (e * N + row) * pitch + col) = fp8_codes16(v, factor);
   }
   if (threadIdx.x == 0) scales[(e * gridDim.y + nb) * gridDim.x + kb] = scale;
 }
 
 template <typename TX>
-static bool fp8_vec(const void* X, int64_t K) {
-  return aligned(X, 16) && (K * static_cast<int64_t>(sizeof(TX))) % 16 == 0;
-}
-
-template <typename TX>
 static hq_status fp8_rows_typed(const void* X, int64_t M, int64_t K, uint8_t* codes, float* scales, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(ceil_div(M, kFp8RowsPerCta)), static_cast<unsigned>(ceil_div(K, kFp8ColsPerWarp)));
-  fp8_rows_kernel<TX><<<grid, 32 * kFp8RowsPerCta, 0, s>>>(static_cast<const TX*>(X), M, K, fp8_pitch(K),
-                                                           fp8_vec<TX>(X, K), codes, scales);
+  const auto kernel = fp8_aligned<TX>(X, K) ? fp8_rows_kernel<true, TX> : fp8_rows_kernel<false, TX>;
+  kernel<<<grid, 256, 0, s>>>(static_cast<const TX*>(X), M, K, fp8_pitch(K), codes, scales);
   HQ_LAUNCH_CHECK();
   return HQ_OK;
 }
@@ -92,8 +103,8 @@ static hq_status fp8_blocks_typed(const void* W, int64_t E, int64_t N, int64_t K
                                   cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(ceil_div(K, kFp8Block)), static_cast<unsigned>(ceil_div(N, kFp8Block)),
                   static_cast<unsigned>(E));
-  fp8_blocks_kernel<TX><<<grid, 256, 0, s>>>(static_cast<const TX*>(W), N, K, fp8_pitch(K), fp8_vec<TX>(W, K), codes,
-                                             scales);
+  const auto kernel = fp8_aligned<TX>(W, K) ? fp8_blocks_kernel<true, TX> : fp8_blocks_kernel<false, TX>;
+  kernel<<<grid, 256, 0, s>>>(static_cast<const TX*>(W), N, K, fp8_pitch(K), codes, scales);
   HQ_LAUNCH_CHECK();
   return HQ_OK;
 }
