@@ -43,8 +43,8 @@ hq_status hq_debug_hessian_accumulate_impl(float* H, const void* X, int x_dtype,
 
 /*
  * hq_fp8_gemm (offsets NULL, E = 1) and hq_fp8_expert_gemm with an explicit kernel choice: impl
- * 0 = automatic, 1 = one CTA per tile, 2 = a pair of CTAs per tile, 3, 4 and 5 = the kernel
- * for few rows with tiles of 16, 32 and 64 rows.
+ * 0 = automatic, 1 = one CTA per tile, 2 = a pair of CTAs per tile, 3 and 4 = the kernel
+ * for few rows with tiles of 16 and 64 rows.
  */
 hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, int64_t rows, const int32_t* offsets,
                                  const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K,

@@ -464,12 +464,19 @@ _FP8 = (torch.float8_e4m3fn, torch.uint8)
 
 def _ptrs(*tensors):
     """The pointers of contiguous tensors (or None) that all live on the current device."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
     ptrs = []
     for t in tensors:
-        ptrs.append(_ptr(t))
-        if t is not None and t.get_device() != dev:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("expected a CUDA tensor")
             raise ValueError(f"expected tensors on the current device (cuda:{dev}), got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        ptrs.append(t.data_ptr())
     return ptrs
 
 

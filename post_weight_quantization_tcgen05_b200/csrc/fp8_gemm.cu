@@ -121,18 +121,29 @@ __device__ __forceinline__ void store_rows(const GemmArgs& a, const CUtensorMap*
       }
     } else {
       __syncwarp();
-      const int p = lane & 7;
-      const int at = col + c + p * kPer;
-      for (int r = lane >> 3; r < 32 && r < rows_left; r += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) << 4));
-        TY* out = static_cast<TY*>(a.Y) + static_cast<int64_t>(row + r) * a.N + at;
-        if (a.y_aligned && at + kPer <= a.N) {
-          *reinterpret_cast<uint4*>(out) = v;
-        } else {
-          const TY* e = reinterpret_cast<const TY*>(&v);
+      TY* out = static_cast<TY*>(a.Y) + static_cast<int64_t>(row) * a.N;
+      if (a.y_aligned) {
+        const int p = lane & 7;
+        const int at = col + c + p * kPer;
+        if (at < a.N)  // whole 16 bytes, as the rows are made of them
+          for (int r = lane >> 3; r < rows_left; r += 4)
+            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * a.N + at) =
+                *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) << 4));
+      } else {
+        // 4 bytes a lane, a row at a time
+        constexpr int kEach = 4 / sizeof(TY);
+        const int at = col + c + lane * kEach;
+        for (int r = 0; r < rows_left && r < 32; ++r) {
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+          TY* o = out + static_cast<int64_t>(r) * a.N + at;
+          if (at + kEach <= a.N && (reinterpret_cast<uintptr_t>(o) & 3) == 0) {
+            *reinterpret_cast<uint32_t*>(o) = v;
+          } else {
+            const TY* e = reinterpret_cast<const TY*>(&v);
 #pragma unroll
-          for (int k = 0; k < kPer; ++k)
-            if (at + k < a.N) out[k] = e[k];
+            for (int k = 0; k < kEach; ++k)
+              if (at + k < a.N) o[k] = e[k];
+          }
         }
       }
       if (lane == 0) ptx::bulk_commit();  // an empty group in the store's place
@@ -446,9 +457,27 @@ hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
 
 namespace {
 
+// Few rows: the kernel that reads the weights once, in tiles of 16 rows up to 16 rows (1 x 5120 x 5120:
+// 9.3 us against 20.0 us of the single CTAs) and of 64 up to 64 (64 x 5120 x 5120: 13 us against 21 us),
+// and up to 128 where its splitting of K is what fills the GPU (128 x 1100 x 1000: 7.8 us against 9.9 us;
+// not 128 x 17408 x 5120: 29 us against 24 us).  Experts go by their average: tiles of 16 up to 12 rows
+// (512 rows, 48 experts 2560 x 5120: 128 us against 131 us), of 64 up to 64 (4096 rows, 64 experts: 185 us
+// against 191 us).  More rows: whichever of the other two has less to do, by its rounds of tiles over the
+// SMs.  A block of 128 columns takes a single CTA 0.42 us, a pair (four times the work) 0.52 us, and a
+// launch about 5 us around them: 384 x 5120 x 5120 23 us against 27 us, 512 39 us against 27 us, 1024
+// 56 us against 48 us, 256 x 17408 x 5120 40 us against 29 us.
 int pick_impl(const Fp8Gemm& p) {
-  const int64_t each = p.rows / p.E;  // rows of an expert, on average
-  return each >= 256 ? kFp8Pair : each > 64 ? kFp8Single : each > 32 ? kFp8Few64 : each > 16 ? kFp8Few32 : kFp8Few16;
+  const bool experts = p.offsets != nullptr;
+  const int64_t each = ceil_div(p.rows, p.E), n128 = ceil_div(p.N, 128);
+  if (each <= (experts ? 12 : 16)) return kFp8Few16;
+  if (each <= 64 || (!experts && each <= 128 && ceil_div(p.rows, 64) * n128 * 8 <= 2 * fp8::kSMs)) return kFp8Few64;
+  // an expert's last tile is half full on average
+  const int64_t m128 = experts ? p.rows / 128 + ceil_div(p.E, 2) : ceil_div(p.rows, 128);
+  const int64_t m256 = experts ? p.rows / 256 + ceil_div(p.E, 2) : ceil_div(p.rows, 256);
+  const int64_t blocks = ceil_div(p.K, kFp8Block);
+  const int64_t single = 500 + 42 * blocks * ceil_div(m128 * n128, fp8::kSMs);
+  const int64_t pair = 600 + 52 * blocks * ceil_div(m256 * ceil_div(p.N, 256), fp8::kSMs / 2);
+  return pair < single ? kFp8Pair : kFp8Single;
 }
 
 }  // namespace
@@ -459,7 +488,6 @@ hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s) {
     case kFp8Pair: return fp8::gemm_pair(p, s);
     case kFp8Single: return fp8::gemm_single(p, s);
     case kFp8Few64: return fp8::gemm_few(p, 64, s);
-    case kFp8Few32: return fp8::gemm_few(p, 32, s);
     default: return fp8::gemm_few(p, 16, s);
   }
 }

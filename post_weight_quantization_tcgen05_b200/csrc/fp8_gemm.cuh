@@ -165,7 +165,7 @@ inline cudaError_t launch_product(const Fp8Gemm& p, void (*kernel)(KArgs...), un
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// fp8_gemm_few.cu: for few rows, in tiles of 16, 32 or 64.  With p.X (few_quantises(p), tiles of 16) the
+// fp8_gemm_few.cu: for few rows, in tiles of 16 or 64.  With p.X (few_quantises(p), tiles of 16) the
 // rows are quantised by the kernel itself.
 bool few_quantises(const Fp8Gemm& p);
 hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s);

@@ -1,8 +1,8 @@
 // The e4m3 product for few rows (a serving step): bound by reading the weights.  The mathematics and
 // the scaling after every block of 128 columns are those of fp8_gemm.cu, with the operands exchanged:
-// 128 rows of W are the MMA's 128 rows, BT rows of A (16, 32 or 64) its columns.  A block's accumulator
-// is then BT columns of tensor memory, so 256 of them hold 16, 8 or 4 accumulators and the hand-over to the
-// epilogue, several hundred cycles, never holds up the loads; a stage takes 16 KB of W and 2 to 8 KB
+// 128 rows of W are the MMA's 128 rows, BT rows of A (16 or 64) its columns.  A block's accumulator is
+// then BT columns of tensor memory, so 256 of them hold 16 or 4 accumulators and the hand-over to the
+// epilogue, several hundred cycles, never holds up the loads; a stage takes 16 KB of W and 2 or 8 KB
 // of A, and two CTAs on an SM keep 10 stages on their way.
 //
 // Where there are fewer tiles than CTAs the GPU holds, a cluster of up to 8 CTAs shares a tile, each
@@ -448,7 +448,6 @@ hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
 template <typename TY>
 hq_status run_few_as(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {
   if (tile_rows == 64) return run_few<64, TY, uint8_t>(p, s);
-  if (tile_rows == 32) return run_few<32, TY, uint8_t>(p, s);
   if (p.X == nullptr) return run_few<16, TY, uint8_t>(p, s);
   return p.x_dtype == HQ_F32 ? run_few<16, TY, float>(p, s) : run_few<16, TY, __nv_bfloat16>(p, s);
 }

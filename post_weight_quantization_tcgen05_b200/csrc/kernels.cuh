@@ -221,7 +221,7 @@ struct Fp8Gemm {
   int x_dtype;
   bool chained;
 };
-enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2, kFp8Few16 = 3, kFp8Few32 = 4, kFp8Few64 = 5 };
+enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2, kFp8Few16 = 3, kFp8Few64 = 4 };
 hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s);
 hq_status launch_fp8_linear(Fp8Gemm p, uint8_t* codes, float* scales, cudaStream_t s);
 
