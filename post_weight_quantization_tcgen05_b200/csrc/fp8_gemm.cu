@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     if constexpr (kPair) ptx::regs_dec<kRegsCtl>();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------------ TMA producer
     ptx::prefetch_tensormap(&mapA);
     ptx::prefetch_tensormap(&mapW);
@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = g > kStages ? g - kStages : 0; k < g; ++k)
           ptx::mbar_wait(&sh.full[k % kStages], (k / kStages) & 1, nullptr);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer
+    const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
     constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kBM, kBN, false, false);
     bool ok = true;
     for (int g = 0; g < blocks; ++g) {
@@ -264,13 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::tc_fence_after();
       const uint32_t dacc = tmem + static_cast<uint32_t>(b * kBN);
-      const uint32_t sa = ptx::smem_u32(smem + s * kStageBytes);
-      const uint32_t sb = sa + kRows * kBK;
+      const uint64_t sd = desc0 + static_cast<uint64_t>(s * (kStageBytes >> 4));
 #pragma unroll
       for (int kk = 0; kk < kBK / 32; ++kk) {
-        // K-major rows of 128 bytes, 8-row groups 1 KB apart (SBO); an MMA takes 32 bytes of each row
-        const uint64_t ad = ptx::sdesc_sw128(sa + kk * 32, 16, 1024);
-        const uint64_t bd = ptx::sdesc_sw128(sb + kk * 32, 16, 1024);
+        const uint64_t ad = sd + kk * 2, bd = sd + kk * 2 + (kRows * kBK >> 4);
         if constexpr (kPair)
           ptx::mma_f8_pair(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
         else

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     ptx::fence_async_smem();  // the codes, to the tensor core
     __syncthreads();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------------ TMA producer
     bool waited = false;
     int g = 0;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       for (int k = g > kStages ? g - kStages : 0; k < g; ++k)
         ptx::mbar_wait(&sh.full[k % kStages], (k / kStages) & 1, nullptr);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kRows, BT, false, false);
     for (int g = 0; g < blocks; ++g) {

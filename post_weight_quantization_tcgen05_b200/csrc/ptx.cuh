@@ -88,6 +88,13 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// True in one lane of a converged warp; the compiler then knows that a single thread runs what follows.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
