@@ -55,8 +55,8 @@ struct Shared {
   Tile places[kPlaces];
   uint64_t full[kStages];   // in a pair the even CTA's: both CTAs' loads
   uint64_t empty[kStages];
-  uint64_t accf[2];         // accumulator filled
-  uint64_t acce[2];         // accumulator drained (in a pair the even CTA's: by both)
+  uint64_t accf[2][2];      // accumulator filled, by half of its columns (one half in a single CTA)
+  uint64_t acce[2][2];      // the same drained (in a pair the even CTA's: by both)
   uint64_t scf[2];          // scales of half the ring written
   uint64_t sce[2];          // scales of half the ring read
   uint64_t drain;
@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap mapY, GemmArgs args) {
   constexpr int kBM = kPair ? 256 : 128, kBN = kPair ? 256 : 128;  // the tile
   constexpr int NC = kBN / 2;                                      // columns of an epilogue warp
+  constexpr int kHalves = kPair ? 2 : 1;                           // accumulators handed over by halves
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stores = smem + kStages * kStageBytes;
@@ -172,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sh.full[s], 1);
       ptx::mbar_init(&sh.empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(&sh.accf[b], 1);
-      ptx::mbar_init(&sh.acce[b], kPair ? 2 * kEpiWarps : kEpiWarps);
+    for (int b = 0; b < 4; ++b) {
+      ptx::mbar_init(&sh.accf[b >> 1][b & 1], 1);
+      ptx::mbar_init(&sh.acce[b >> 1][b & 1], kEpiWarps);  // of a pair: half the warps of two CTAs
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&sh.scf[s], 1);
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < own && ok; ++i) {
       const Tile x = tile_at<kBM, kBN>(args, sh.start, first + i * step);
       const int a_row = x.m0 + rank * kRows;
-      const int w_row = x.e * args.N + x.n0 + rank * kRows;
+      const int w_row = x.e * args.N + x.n0 + rank * 64;
       (void)HQ_IN_BOUNDS(x.m0 < args.rows && x.n0 < args.N);
       for (int k = 0; k < args.kblocks; ++k, ++g) {
         const int s = g % kStages;
@@ -236,7 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) ptx::mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
           const uint32_t bar = ptx::mapa(&sh.full[s], 0);
           ptx::tma_load_2d_pair(sa, &mapA, k * kBK, a_row, bar);
+          // 64 rows for each half of the tile's columns
           ptx::tma_load_2d_pair(sa + kRows * kBK, &mapW, k * kBK, w_row, bar);
+          ptx::tma_load_2d_pair(sa + (kRows + 64) * kBK, &mapW, k * kBK, w_row + 128, bar);
         } else {
           ptx::mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
           ptx::tma_load_2d(sa, &mapA, k * kBK, a_row, &sh.full[s]);
@@ -254,33 +257,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 && rank == 0 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
-    constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kBM, kBN, false, false);
+    constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kBM, kBN / kHalves, false, false);
     bool ok = true;
-    for (int g = 0; g < blocks; ++g) {
+    for (int g = 0; g < blocks && ok; ++g) {
       const int s = g % kStages, b = g & 1;
-      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag) ||
-          (g >= 2 && !ptx::mbar_wait(&sh.acce[b], ((g >> 1) - 1) & 1, abort_flag))) {
+      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag)) {
         ok = false;
         break;
       }
-      ptx::tc_fence_after();
-      const uint32_t dacc = tmem + static_cast<uint32_t>(b * kBN);
-      const uint64_t sd = desc0 + static_cast<uint64_t>(s * (kStageBytes >> 4));
 #pragma unroll
-      for (int kk = 0; kk < kBK / 32; ++kk) {
-        const uint64_t ad = sd + kk * 2, bd = sd + kk * 2 + (kRows * kBK >> 4);
+      for (int h = 0; h < kHalves; ++h) {
+        if (g >= 2 && !ptx::mbar_wait(&sh.acce[b][h], ((g >> 1) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t dacc = tmem + static_cast<uint32_t>(b * kBN + h * 128);
+        // K-major rows of 128 bytes, 8-row groups 1 KB apart (SBO); an MMA takes 32 bytes of each row
+        const uint64_t sd = desc0 + static_cast<uint64_t>(s * (kStageBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk) {
+          const uint64_t ad = sd + kk * 2, bd = sd + kk * 2 + ((kRows + h * 64) * kBK >> 4);
+          if constexpr (kPair)
+            ptx::mma_f8_pair(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
+          else
+            ptx::mma_f8(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
+        }
         if constexpr (kPair)
-          ptx::mma_f8_pair(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
+          ptx::mma_commit_pair(&sh.accf[b][h]);
         else
-          ptx::mma_f8(dacc, ad, bd, kIdesc, kk > 0 ? 1u : 0u);
+          ptx::mma_commit(&sh.accf[b][h]);
       }
-      if constexpr (kPair) {
-        ptx::mma_commit_pair(&sh.accf[b]);
+      if (!ok) break;
+      if constexpr (kPair)
         ptx::mma_commit_pair(&sh.empty[s]);
-      } else {
-        ptx::mma_commit(&sh.accf[b]);
+      else
         ptx::mma_commit(&sh.empty[s]);
-      }
     }
     if (!ok) {
       fail();
@@ -353,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (warp - 4) >> 2;  // which half of the tile's columns
     const uint32_t tmem_w = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * NC);
     uint8_t* stage = stores + (warp - 4) * kStoreBytes;
-    const uint32_t acce = kPair ? ptx::mapa(&sh.acce[0], 0) : ptx::smem_u32(&sh.acce[0]);
+    const int half = kPair ? h : 0;
+    const uint32_t acce = kPair ? ptx::mapa(&sh.acce[0][half], 0) : ptx::smem_u32(&sh.acce[0][half]);
     const uint32_t sce = ptx::smem_u32(&sh.sce[0]);
     const uint32_t scale_at = ptx::smem_u32(&sh.scales[0][h][q * 32 + lane]);
     bool ok = true, seen = false;  // seen: the block's accumulator has been seen filled
@@ -370,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         if (!__all_sync(0xffffffffu, seen)) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.accf[b], (g >> 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.accf[b][half], (g >> 1) & 1, abort_flag));
           if (!ok) break;
         }
         ptx::tc_fence_after();
@@ -394,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        ptx::mbar_arrive_cluster(acce + 8 * b, lane == 0);
+        ptx::mbar_arrive_cluster(acce + 16 * b, lane == 0);
         ptx::mbar_arrive_cluster(sce + 8 * ((g / kScaleHalf) & 1), lane == 0 && g % kScaleHalf == kScaleHalf - 1);
-        seen = ptx::mbar_test(&sh.accf[b ^ 1], ((g + 1) >> 1) & 1);
+        seen = ptx::mbar_test(&sh.accf[b ^ 1][half], ((g + 1) >> 1) & 1);
         add(NC / 32 - 2);
         add(NC / 32 - 1);
       }
@@ -427,7 +440,7 @@ hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
   const int64_t most = most_tiles(p, kTile, kTile);
   CUtensorMap map_a, map_w, map_y;
   GemmArgs a{};
-  const hq_status st = gemm_args(p, most, kRows, kRows, a, map_a, map_w);
+  const hq_status st = gemm_args(p, most, kRows, kPair ? 64 : kRows, a, map_a, map_w);
   if (st != HQ_OK) return st;
   if (!a.y_aligned)
     map_y = map_a;  // not used
