@@ -487,6 +487,11 @@ def _want(t, name: str, dtype, shape) -> None:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
 
 
+def _want_status(dev_status) -> None:
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.numel() < 1):
+        raise ValueError("dev_status must be an int32 tensor")
+
+
 def _blocks(n: int) -> int:
     return (n + 127) // 128
 
@@ -528,6 +533,7 @@ def hq_fp8_gemm(a_codes, a_scales, w_codes, w_scales, K: int, Y, dev_status=None
     _want(a_scales, "a_scales", torch.float32, (_blocks(K), M))
     _want(w_codes, "w_codes", _FP8, (N, _pitch(K)))
     _want(w_scales, "w_scales", torch.float32, (_blocks(N), _blocks(K)))
+    _want_status(dev_status)
     a, sa, w, sw, y, st = _ptrs(a_codes, a_scales, w_codes, w_scales, Y, dev_status)
     _check(lib.hq_fp8_gemm(a, sa, M, w, sw, N, K, y, _dtype(Y), st, _stream(stream)), "hq_fp8_gemm")
 
@@ -544,6 +550,7 @@ def hq_fp8_linear(X, w_codes, w_scales, Y, workspace, dev_status=None, stream=No
     _want(w_scales, "w_scales", torch.float32, (_blocks(N), _blocks(K)))
     if tuple(Y.shape) != (M, N):
         raise ValueError(f"Y must have shape {(M, N)}, not {tuple(Y.shape)}")
+    _want_status(dev_status)
     x, w, sw, y, ws, st = _ptrs(X, w_codes, w_scales, Y, workspace, dev_status)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.hq_fp8_linear(x, _dtype(X), M, w, sw, N, K, y, _dtype(Y), ws, nbytes, st, _stream(stream)),
@@ -560,6 +567,7 @@ def hq_fp8_expert_gemm(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y,
     _want(offsets, "offsets", torch.int32, (E + 1,))
     _want(w_codes, "w_codes", _FP8, (E, N, _pitch(K)))
     _want(w_scales, "w_scales", torch.float32, (E, _blocks(N), _blocks(K)))
+    _want_status(dev_status)
     a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
     _check(lib.hq_fp8_expert_gemm(a, sa, rows, off, w, sw, E, N, K, y, _dtype(Y), st, _stream(stream)),
            "hq_fp8_expert_gemm")
@@ -569,6 +577,7 @@ def hq_debug_fp8_gemm_impl(a_codes, a_scales, offsets, w_codes, w_scales, K: int
                            stream=None) -> None:
     """hq_fp8_gemm (offsets None) or hq_fp8_expert_gemm by a chosen kernel (hq_debug.h)."""
     rows, N = Y.shape
+    _want_status(dev_status)
     a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
     _check(lib.hq_debug_fp8_gemm_impl(a, sa, rows, off, w, sw, 1 if offsets is None else w_codes.shape[0], N, K, y,
                                       _dtype(Y), st, int(impl), _stream(stream)), "hq_debug_fp8_gemm_impl")

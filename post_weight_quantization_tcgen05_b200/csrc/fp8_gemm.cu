@@ -8,6 +8,13 @@
 // registers.  So the accumulator restarts at every block, and the epilogue warps read and scale
 // one while the tensor core fills the other (two accumulators).
 //
+// What bounds it: the hand-over of the accumulators.  Of a pair's block of 128 columns the MMAs alone, with
+// their loads, take 675 cycles (8192 x 17408 x 5120: 412 us, 3.5 PFLOP/s; shared memory moves 64 KB a block
+// and SM at 128 bytes a cycle); a signal from the MMAs to the epilogue or back takes about 400 cycles,
+// reading an accumulator 400.  With two whole accumulators that came to 1040 cycles (645 us); handed over
+// by halves of 128 columns the two halves' hand-overs overlap each other's MMAs, which then read A's
+// operand twice: 607 us, 2.4 PFLOP/s.
+//
 // Two tilings of one kernel:
 //   pair   : two CTAs (a cluster) compute a 256 x 256 tile with cta_group::2 MMAs, each of them 128
 //            rows.  On one SM a 128 x 256 tile takes 48 KB of operands for every 512 cycles of
@@ -469,25 +476,26 @@ hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
 namespace {
 
 // Few rows: the kernel that reads the weights once, in tiles of 16 rows up to 16 rows (1 x 5120 x 5120:
-// 9.3 us against 20.0 us of the single CTAs) and of 64 up to 64 (64 x 5120 x 5120: 13 us against 21 us),
-// and up to 128 where its splitting of K is what fills the GPU (128 x 1100 x 1000: 7.8 us against 9.9 us;
-// not 128 x 17408 x 5120: 29 us against 24 us).  Experts go by their average: tiles of 16 up to 12 rows
-// (512 rows, 48 experts 2560 x 5120: 128 us against 131 us), of 64 up to 64 (4096 rows, 64 experts: 185 us
-// against 191 us).  More rows: whichever of the other two has less to do, by its rounds of tiles over the
-// SMs.  A block of 128 columns takes a single CTA 0.42 us, a pair (four times the work) 0.52 us, and a
-// launch about 5 us around them: 384 x 5120 x 5120 23 us against 27 us, 512 39 us against 27 us, 1024
-// 56 us against 48 us, 256 x 17408 x 5120 40 us against 29 us.
+// 9.1 us against 16 us of the single CTAs) and of 64 up to 64 (33 x 5120 x 5120: 12.7 us against 13.9 us
+// with tiles of 16 and 16.3 us of the single CTAs, 64 14.8 us against 16.8 us and 16.5 us; 96 22 us against
+// 17 us).  Experts go by their average, as their sizes differ: tiles of 16 up to 24 rows (800 rows, 48
+// experts 2560 x 5120: 100 us against 109 us with tiles of 64; 2048 rows, 64 experts 164 us against
+// 153 us), of 64 up to 48 (2048 rows: 153 us against 167 us of the single CTAs; 4096 218 us against
+// 194 us).  More rows: whichever of the other two has less to do, by its rounds of tiles over the SMs.
+// A block of 128 columns takes a single CTA 0.32 us, a pair (four times the work) 0.47 us, and a launch
+// 5 or 6 us around them: 384 x 5120 x 5120 18 us against 24 us, 768 31 us against 25 us, 1024 43 us
+// either way, 2048 69 us against 61 us, 256 x 17408 x 5120 34 us against 26 us.
 int pick_impl(const Fp8Gemm& p) {
   const bool experts = p.offsets != nullptr;
-  const int64_t each = ceil_div(p.rows, p.E), n128 = ceil_div(p.N, 128);
-  if (each <= (experts ? 12 : 16)) return kFp8Few16;
-  if (each <= 64 || (!experts && each <= 128 && ceil_div(p.rows, 64) * n128 * 8 <= 2 * fp8::kSMs)) return kFp8Few64;
+  const int64_t each = ceil_div(p.rows, p.E);
+  if (each <= (experts ? 24 : 16)) return kFp8Few16;
+  if (each <= (experts ? 48 : 64)) return kFp8Few64;
   // an expert's last tile is half full on average
   const int64_t m128 = experts ? p.rows / 128 + ceil_div(p.E, 2) : ceil_div(p.rows, 128);
   const int64_t m256 = experts ? p.rows / 256 + ceil_div(p.E, 2) : ceil_div(p.rows, 256);
   const int64_t blocks = ceil_div(p.K, kFp8Block);
-  const int64_t single = 500 + 42 * blocks * ceil_div(m128 * n128, fp8::kSMs);
-  const int64_t pair = 600 + 52 * blocks * ceil_div(m256 * ceil_div(p.N, 256), fp8::kSMs / 2);
+  const int64_t single = 500 + 32 * blocks * ceil_div(m128 * ceil_div(p.N, 128), fp8::kSMs);
+  const int64_t pair = 600 + 47 * blocks * ceil_div(m256 * ceil_div(p.N, 256), fp8::kSMs / 2);
   return pair < single ? kFp8Pair : kFp8Single;
 }
 

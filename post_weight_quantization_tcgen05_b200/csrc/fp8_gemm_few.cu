@@ -388,44 +388,46 @@ constexpr int kSlots = kSMs * kCtasPerSM;
 
 // How many clusters of `split` CTAs the current device holds at once, asked once: a cluster lies within
 // one GPC, so it depends on how many SMs each of the chip's GPCs has (40 clusters of 7 did not fit at
-// once although their 280 CTAs are fewer than 296, and 5120 x 5120 took 15.8 us instead of 9.9).
-template <typename Kernel>
-int clusters_at_once(Kernel kernel, int smem, int split) {
-  static std::atomic<int> known[kMaxSplit + 1];  // one per kernel
+// once although their 280 CTAs are fewer than 296, and 5120 x 5120 took 15.8 us instead of 9.9).  Asked of
+// the variant that takes most shared memory, so that all variants of a tile height split alike and their
+// sums are the same; the device is assumed to be like the first one asked.  0: not known.
+template <int BT>
+int clusters_at_once(int split) {
+  using TX = typename std::conditional<BT == 16, __nv_bfloat16, uint8_t>::type;
+  static std::atomic<int> known[kMaxSplit + 1];
   int n = known[split].load(std::memory_order_relaxed);
-  if (n != 0) return n;
+  if (n > 0) return n;
+  const auto kernel = fp8_gemm_few_kernel<BT, __nv_bfloat16, TX>;
+  constexpr int kSmem = Few<BT, BT == 16>::kSmem;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.dynamicSmemBytes = kSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(split);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
-    n = 0;
+    return 0;
   }
-  if (n < 1) n = 1;
   known[split].store(n, std::memory_order_relaxed);
   return n;
 }
 
-template <int BT, typename TY, typename TX>
-struct Launch {
-  static constexpr int kSmem = Few<BT, !std::is_same<TX, uint8_t>::value>::kSmem;
-  // CTAs to a tile: as many as leave all tiles' clusters on the GPU at once, where the number of tiles is
-  // known (one weight).  The device is assumed to be like the first one asked.
-  static int split(const Fp8Gemm& p) {
-    const int64_t tiles = ceil_div(p.rows, BT) * ceil_div(p.N, kRows);
-    if (p.offsets != nullptr || tiles * 2 > kSlots) return 1;
-    for (int n = static_cast<int>(std::min<int64_t>({kMaxSplit, kSlots / tiles, ceil_div(p.K, kFp8Block)})); n > 1; --n)
-      if (tiles <= clusters_at_once(fp8_gemm_few_kernel<BT, TY, TX>, kSmem, n)) return n;
-    return 1;
-  }
-};
+// CTAs to a tile: as many as leave all tiles' clusters on the GPU at once, where the number of tiles is
+// known (one weight).
+template <int BT>
+int pick_split(const Fp8Gemm& p) {
+  const int64_t tiles = ceil_div(p.rows, BT) * ceil_div(p.N, kRows);
+  if (p.offsets != nullptr || tiles * 2 > kSlots) return 1;
+  for (int n = static_cast<int>(std::min<int64_t>({kMaxSplit, kSlots / tiles, ceil_div(p.K, kFp8Block)})); n > 1; --n)
+    if (tiles <= clusters_at_once<BT>(n)) return n;
+  return 1;
+}
 
 template <int BT, typename TY, typename TX>
 hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
@@ -434,10 +436,10 @@ hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
   GemmArgs a{};
   const hq_status st = gemm_args(p, most, BT, kRows, a, map_a, map_w);
   if (st != HQ_OK) return st;
-  constexpr int kSmem = Launch<BT, TY, TX>::kSmem;
+  constexpr int kSmem = Few<BT, !std::is_same<TX, uint8_t>::value>::kSmem;
   const auto kernel = fp8_gemm_few_kernel<BT, TY, TX>;
   HQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  const int split = Launch<BT, TY, TX>::split(p);
+  const int split = pick_split<BT>(p);
   const int64_t clusters = split > 1 ? ceil_div(p.rows, BT) * ceil_div(p.N, kRows) : std::min<int64_t>(most, kSlots);
   HQ_LAUNCH_CHAINED(launch_product(p, kernel, static_cast<unsigned>(clusters * split), kThreads, kSmem,
                                    static_cast<unsigned>(split), s, map_a, map_w, a, split,
@@ -452,20 +454,11 @@ hq_status run_few_as(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {
   return p.x_dtype == HQ_F32 ? run_few<16, TY, float>(p, s) : run_few<16, TY, __nv_bfloat16>(p, s);
 }
 
-template <typename TY, typename TX>
-int panel_blocks(const Fp8Gemm& p) {
-  return static_cast<int>(ceil_div(ceil_div(p.K, kFp8Block), Launch<16, TY, TX>::split(p)));
-}
-
 }  // namespace
 
 bool few_quantises(const Fp8Gemm& p) {
-  if (p.offsets != nullptr || p.rows > 4 || ceil_div(p.N, kRows) > kSlots) return false;
-  const bool x32 = p.x_dtype == HQ_F32;
-  const int n = p.y_dtype == HQ_F32
-                    ? (x32 ? panel_blocks<float, float>(p) : panel_blocks<float, __nv_bfloat16>(p))
-                    : (x32 ? panel_blocks<__nv_bfloat16, float>(p) : panel_blocks<__nv_bfloat16, __nv_bfloat16>(p));
-  return n <= kPanel;
+  return p.offsets == nullptr && p.rows <= 4 && ceil_div(p.N, kRows) <= kSlots &&
+         ceil_div(ceil_div(p.K, kFp8Block), pick_split<16>(p)) <= kPanel;
 }
 
 hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {

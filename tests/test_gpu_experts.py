@@ -261,6 +261,37 @@ def test_positions_out_of_range_count_as_dropped(hq, cuda_device):
     assert torch.equal(d[0][0], d[1][0]) and torch.equal(d[0][1], d[1][1])
 
 
+def test_rows_past_2_to_the_31_elements(hq, cuda_device):
+    T, top, E, K = 70_000, 4, 5, 8192
+    assert T * top * K > 2 ** 31
+    ids = choices(3, T, top, E)
+    offsets, order, position = sort(hq, ids, E)
+    n = int(offsets[-1])
+    X = torch.randn((T, K), generator=gen(1), device="cuda").to(torch.bfloat16)
+    w = torch.rand((T, top), generator=gen(2), device="cuda")
+    rows = torch.empty((T * top, K), dtype=X.dtype, device="cuda")
+    hq.hq_expert_dispatch(X, position, rows)
+    some = torch.cat([torch.arange(0, 50), torch.arange(n - 50, n)]).cuda()
+    assert torch.equal(rows[some], X[order[some].long() // top])
+    Y, dX = torch.empty_like(X), torch.empty_like(X)
+    hq.hq_expert_combine(rows, position, None, Y)  # a power of two of a bf16 value where all choices are kept
+    kept = (position >= 0).sum(1)
+    assert torch.equal(Y[kept == 4], (X[kept == 4].float() * 4).to(X.dtype))
+    assert torch.equal(Y[kept == 0], torch.zeros_like(X[kept == 0]))
+    d_rows, d_w = torch.empty_like(rows), torch.empty_like(w)
+    hq.hq_expert_combine_backward(X, rows, position, w, d_rows, d_w)
+    t = order[some].long() // top
+    assert torch.equal(d_rows[some], (X[t].float() * w.reshape(-1)[order[some].long()][:, None]).to(X.dtype))
+    sq = (X[t].double() ** 2).sum(1)
+    assert ((d_w.reshape(-1)[order[some].long()] - sq).abs() <= sq * K * 2.0 ** -24).all()
+    del d_rows, dX, Y
+    codes, scales = hq.fp8_rows_outputs(T * top, K)
+    hq.hq_expert_dispatch_fp8(X, position, codes, scales)
+    ref, ref_s = hq.fp8_rows_outputs(100, K)
+    hq.hq_fp8_quantize_rows(rows[some].contiguous(), ref, ref_s)
+    assert torch.equal(codes.view(torch.uint8)[some], ref.view(torch.uint8)) and torch.equal(scales[:, some], ref_s)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("K", [256, 100])

@@ -336,7 +336,8 @@ IMPLS = {"single": 1, "pair": 2, "few16": 3, "few64": 4}
 
 
 @pytest.mark.parametrize("impl", list(IMPLS))
-@pytest.mark.parametrize("M,N,K", SHAPES + [(2900, 3400, 400), (512, 17408, 256), (16, 5120, 5120), (5, 17408, 640), (64, 4000, 1536)])
+@pytest.mark.parametrize("M,N,K", SHAPES + [(2900, 3400, 400), (512, 17408, 256), (16, 5120, 5120), (5, 17408, 640), (64, 4000, 1536),
+                                             (300, 8, 200), (4000, 4096, 100), (3000, 5000, 129)])
 def test_every_kernel_on_one_weight(hq, cuda_device, M, N, K, impl):
     a, sa = small_integers(1, M, K, 1)
     w, sw = small_integers(2, N, K, 128)
@@ -354,7 +355,8 @@ def test_every_kernel_on_one_weight(hq, cuda_device, M, N, K, impl):
 @pytest.mark.parametrize("impl", list(IMPLS))
 @pytest.mark.parametrize("sizes,gaps,N,K", [([1], (0, 0), 64, 64), ([0, 5, 0, 0, 130, 1, 0], (0, 0), 130, 200),
                                             ([3, 0, 300], (2, 5), 257, 300), ([0, 0, 0], (0, 7), 64, 64),
-                                            ([700, 2, 900], (1, 0), 384, 512), ([257, 0, 1, 255, 256] * 8, (0, 9), 640, 260)])
+                                            ([700, 2, 900], (1, 0), 384, 512), ([257, 0, 1, 255, 256] * 8, (0, 9), 640, 260),
+                                            ([130, 3, 0, 40] * 40, (0, 0), 900, 128)])
 def test_every_kernel_on_experts(hq, cuda_device, sizes, gaps, N, K, impl):
     E = len(sizes)
     offsets, rows = expert_case(0, sizes, gaps, N, K)
@@ -372,3 +374,75 @@ def test_every_kernel_on_experts(hq, cuda_device, sizes, gaps, N, K, impl):
         ref[off[e]:off[e + 1]] = A[off[e]:off[e + 1]] @ W.t()
     assert torch.equal(Y.double(), ref)
     assert status.item() == 0
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_more_than_2_to_the_31_elements(hq, cuda_device):
+    """X, its codes and Y each have more than 2^31 elements: the last rows are what a call of their own
+    makes of them."""
+    M, N, K = 265_000, 8200, 8192
+    assert M * K > 2 ** 31 and M * N > 2 ** 31
+    few = activations(1, 300, K, "bf16")
+    X = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    X[-300:] = few
+    a, sa = quantise_rows(hq, X)
+    del X
+    b, sb = quantise_rows(hq, few)
+    assert torch.equal(a.view(torch.uint8)[-300:], b.view(torch.uint8)) and torch.equal(sa[:, -300:], sb)
+    assert not sa[:, :-300].any()
+    w, sw = quantise_blocks(hq, activations(2, N, K, "bf16"))
+    Y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    hq.hq_fp8_gemm(a, sa, w, sw, K, Y)
+    Z = torch.empty((300, N), dtype=torch.bfloat16, device="cuda")
+    # the same kernel as for the long call, so that the same sums are taken
+    hq.hq_debug_fp8_gemm_impl(b, sb, None, w, sw, K, Z, IMPLS["pair"])
+    assert torch.equal(Y[-300:], Z)
+    assert not Y[:-300].any()
+
+
+def test_a_first_call_under_capture(cuda_device):
+    """A process whose first call of the kernels is captured into a graph."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, post_weight_quantization_tcgen05_b200 as hq
+torch.cuda.init()
+X = torch.ones((300, 256), device="cuda"); w, sw = hq.fp8_blocks_outputs(384, 256); Y = torch.zeros((300, 384), device="cuda")
+W = torch.ones((384, 256), device="cuda"); ws = hq.alloc_workspace(hq.hq_fp8_linear_workspace_bytes(300, 256))
+x = torch.ones((1, 256), device="cuda"); y = torch.zeros((1, 384), device="cuda")
+torch.cuda.synchronize(); g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    hq.hq_fp8_quantize_blocks(W, w, sw)
+    hq.hq_fp8_linear(X, w, sw, Y, ws)
+    hq.hq_fp8_linear(x, w, sw, y, ws)
+g.replay(); torch.cuda.synchronize()
+# 1.0 is quantised to 448 with the scale fp32(1 / 448)
+assert (Y - 256).abs().max() < 256 * 2 ** -20 and (y - 256).abs().max() < 256 * 2 ** -20, (Y.max(), y.max())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_linear_is_the_gemm_of_the_quantised_rows_in_any_order_of_first_calls(cuda_device):
+    """How K is split must not depend on which of the two a process calls first."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, post_weight_quantization_tcgen05_b200 as hq
+for M, N, K in ((1, 200, 300), (2, 200, 300), (1, 5120, 640), (4, 1000, 1000), (1, 640, 5120), (16, 640, 2000)):
+    g = torch.Generator(device="cuda"); g.manual_seed(M + N)
+    X = torch.randn((M, K), device="cuda", generator=g); W = torch.randn((N, K), device="cuda", generator=g)
+    w, sw = hq.fp8_blocks_outputs(N, K); hq.hq_fp8_quantize_blocks(W, w, sw)
+    Y, Z = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+    hq.hq_fp8_linear(X, w, sw, Y, hq.alloc_workspace(hq.hq_fp8_linear_workspace_bytes(M, K)))
+    a, sa = hq.fp8_rows_outputs(M, K); hq.hq_fp8_quantize_rows(X, a, sa)
+    hq.hq_fp8_gemm(a, sa, w, sw, K, Z)
+    assert torch.equal(Y, Z), (M, N, K)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
