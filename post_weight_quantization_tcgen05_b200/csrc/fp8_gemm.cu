@@ -475,21 +475,22 @@ hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
 
 namespace {
 
-// Few rows: the kernel that reads the weights once, in tiles of 16 rows up to 16 rows (1 x 5120 x 5120:
-// 9.1 us against 16 us of the single CTAs) and of 64 up to 64 (33 x 5120 x 5120: 12.7 us against 13.9 us
-// with tiles of 16 and 16.3 us of the single CTAs, 64 14.8 us against 16.8 us and 16.5 us; 96 22 us against
-// 17 us).  Experts go by their average, as their sizes differ: tiles of 16 up to 24 rows (800 rows, 48
-// experts 2560 x 5120: 100 us against 109 us with tiles of 64; 2048 rows, 64 experts 164 us against
-// 153 us), of 64 up to 48 (2048 rows: 153 us against 167 us of the single CTAs; 4096 218 us against
-// 194 us).  More rows: whichever of the other two has less to do, by its rounds of tiles over the SMs.
-// A block of 128 columns takes a single CTA 0.32 us, a pair (four times the work) 0.47 us, and a launch
-// 5 or 6 us around them: 384 x 5120 x 5120 18 us against 24 us, 768 31 us against 25 us, 1024 43 us
-// either way, 2048 69 us against 61 us, 256 x 17408 x 5120 34 us against 26 us.
+// Few rows: the kernel that reads the weights once, in tiles of 16 rows up to 32 rows (1 x 5120 x 5120:
+// 9 us against 18 us of the single CTAs; 24 x 17408 x 5120: 20.1 us against 23.5 us with tiles of 64, the
+// second tile's weights coming from L2) and of 64 up to 64 where the single CTAs' tiles would leave half
+// the SMs idle (64 x 5120 x 5120: 14.8 us against 18.2 us, 64 x 5120 x 17408: 25 us against 50 us; not
+// 64 x 17408 x 5120: 27 us against 21 us).  Experts go by their average, as their sizes differ: tiles of 16
+// up to 24 rows (800 rows, 48 experts 2560 x 5120: 100 us against 109 us with tiles of 64; 2048 rows, 64
+// experts 164 us against 153 us), of 64 up to 48 (2048 rows: 153 us against 167 us of the single CTAs;
+// 4096 218 us against 194 us).  More rows: whichever of the other two has less to do, by its rounds of
+// tiles over the SMs.  A block of 128 columns takes a single CTA 0.32 us, a pair (four times the work)
+// 0.47 us, and a launch 5 or 6 us around them: 384 x 5120 x 5120 18 us against 24 us, 768 31 us against
+// 25 us, 1024 43 us either way, 2048 69 us against 61 us, 256 x 17408 x 5120 34 us against 26 us.
 int pick_impl(const Fp8Gemm& p) {
   const bool experts = p.offsets != nullptr;
   const int64_t each = ceil_div(p.rows, p.E);
-  if (each <= (experts ? 24 : 16)) return kFp8Few16;
-  if (each <= (experts ? 48 : 64)) return kFp8Few64;
+  if (each <= (experts ? 24 : 32)) return kFp8Few16;
+  if (experts ? each <= 48 : each <= 64 && ceil_div(p.N, 128) * 2 <= fp8::kSMs) return kFp8Few64;
   // an expert's last tile is half full on average
   const int64_t m128 = experts ? p.rows / 128 + ceil_div(p.E, 2) : ceil_div(p.rows, 128);
   const int64_t m256 = experts ? p.rows / 256 + ceil_div(p.E, 2) : ceil_div(p.rows, 256);

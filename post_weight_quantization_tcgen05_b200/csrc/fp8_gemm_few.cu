@@ -43,7 +43,7 @@ constexpr int kFetch = kScaleHalf;
 constexpr int kPlaces = 16;
 static_assert(kPlaces > kScales + kFetch, "a tile's place is overwritten after the epilogue read it");
 
-constexpr int kPanel = 20;  // blocks of A that a CTA quantises and keeps
+constexpr int kPanel = 16;  // blocks of A that a CTA quantises and keeps
 
 template <int BT, bool kQuantise>
 struct Shared {
@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     const int q = warp & 3;  // TMEM lane quadrant this warp may access
     const uint32_t tmem_w = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int n = q * 32 + lane;  // this thread's row of the tile's 128 of W
-    int g = 0;
+    constexpr int kStep = BT < 32 ? BT : 32;
+    int g = 0, left = 0;
     for (int i = 0; i < own && ok; ++i) {
       float acc[BT];
 #pragma unroll
@@ -313,18 +314,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
         ptx::tc_fence_after();
         const float4* scale = reinterpret_cast<const float4*>(sh.scales[kQuantise ? g : g % kScales]);
         const uint32_t from = tmem_w + static_cast<uint32_t>(b * BT);
+        if (k == 0) left = sh.places[i % kPlaces].m1 - sh.places[i % kPlaces].m0;
 #pragma unroll
-        for (int c = 0; c < BT; c += 16) {
-          uint32_t r[16];
-          ptx::tmem_ld16_nowait(from + c, r);
+        for (int c = 0; c < BT; c += kStep) {
+          if (c >= left) break;  // rows that the tile does not have
+          uint32_t r[kStep];
+          if constexpr (kStep == 16)
+            ptx::tmem_ld16_nowait(from + c, r);
+          else
+            ptx::tmem_ld32_nowait(from + c, r);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < kStep; j += 4) {
             const float4 sc = scale[(c + j) / 4];
-            acc[c + j] = fmaf(sc.x, __uint_as_float(r[j]), acc[c + j]);
-            acc[c + j + 1] = fmaf(sc.y, __uint_as_float(r[j + 1]), acc[c + j + 1]);
-            acc[c + j + 2] = fmaf(sc.z, __uint_as_float(r[j + 2]), acc[c + j + 2]);
-            acc[c + j + 3] = fmaf(sc.w, __uint_as_float(r[j + 3]), acc[c + j + 3]);
+            ptx::fma2(acc[c + j], acc[c + j + 1], sc.x, sc.y, r[j], r[j + 1]);
+            ptx::fma2(acc[c + j + 2], acc[c + j + 3], sc.z, sc.w, r[j + 2], r[j + 3]);
           }
         }
         ptx::tc_fence_before();
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       }
       if (!ok) break;
       const Tile x = sh.places[i % kPlaces];
-      const int col = x.n0 + n, left = x.m1 - x.m0;
+      const int col = x.n0 + n;
       if (split == 1) {
         TY* y = static_cast<TY*>(args.Y) + static_cast<int64_t>(x.m0) * args.N + col;
         if (col < args.N && HQ_IN_BOUNDS(x.m0 >= 0 && x.m1 <= args.rows)) {
@@ -390,7 +394,9 @@ constexpr int kSlots = kSMs * kCtasPerSM;
 // one GPC, so it depends on how many SMs each of the chip's GPCs has (40 clusters of 7 did not fit at
 // once although their 280 CTAs are fewer than 296, and 5120 x 5120 took 15.8 us instead of 9.9).  Asked of
 // the variant that takes most shared memory, so that all variants of a tile height split alike and their
-// sums are the same; the device is assumed to be like the first one asked.  0: not known.
+// sums are the same; the device is assumed to be like the first one asked.  The runtime counts one CTA an
+// SM for kernels that allocate tensor memory; two of these run there (240 CTAs in clusters of 6 were seen
+// at once, 272 of 2), so its count is taken up by that.  0: not known.
 template <int BT>
 int clusters_at_once(int split) {
   using TX = typename std::conditional<BT == 16, __nv_bfloat16, uint8_t>::type;
@@ -409,11 +415,14 @@ int clusters_at_once(int split) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  int counted = 0;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&counted, kernel, kThreads, kSmem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;
   }
+  if (counted == 1) n *= kCtasPerSM;
   known[split].store(n, std::memory_order_relaxed);
   return n;
 }

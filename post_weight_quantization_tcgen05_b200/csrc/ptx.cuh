@@ -307,6 +307,15 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float s, uint32_t v0,
       : "f"(s), "f"(__uint_as_float(v0)), "f"(__uint_as_float(v1)));
 }
 
+// (d0, d1) += (s0, s1) (v0, v1)
+__device__ __forceinline__ void fma2(float& d0, float& d1, float s0, float s1, uint32_t v0, uint32_t v1) {
+  asm("{\n\t.reg .b64 d, a, b;\n\t"
+      "mov.b64 d, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(s0), "f"(s1), "f"(__uint_as_float(v0)), "f"(__uint_as_float(v1)));
+}
+
 // 32 lanes x 16 consecutive 32-bit columns: thread t of the warp receives TMEM lane
 // (lane_base + t), columns [col, col+16).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
