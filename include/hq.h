@@ -354,14 +354,18 @@ hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t 
  *   NULL is accepted where that size is 0.
  * hq_fp8_expert_gemm: rows offsets[e] .. offsets[e + 1] - 1 of A and Y meet weight e of W
  *   [E, N, K], for every expert.  offsets: DEVICE int32 [E + 1], not decreasing, between 0 and
- *   `rows` (a range outside is cut to it, an inverted one is empty).  Rows of Y outside every range
+ *   `rows` (a range outside is cut to it, an inverted one is empty, and rows that ranges share hold
+ *   the result of any of them, or what they held).  Rows of Y outside every range
  *   are left as they were; an expert without rows costs nothing.
  * A NaN or infinity in a row of A reaches that row of Y only, one in W's block the columns of its
  * 128 rows.  A row's result does not depend on the other rows' values, and is identical run to run.
  *   dev_status : optional device int; if non-NULL a kernel that hits a bounded-wait timeout stores
  *            HQ_ERR_TIMEOUT there (the caller zeroes it beforehand).
- * Asynchronous.  Y must not alias the operands.  Sizes as for the quantisers.  There is no gradient
- * here: the codes are whole numbers of a layer that has been trained.
+ * sa sw is formed in fp32: where it is below 2^-126 the block's sum loses bits, where it overflows
+ * the result is not finite.
+ * Asynchronous.  Y must not alias the operands.  Sizes as for the quantisers; a product of 2^31 or
+ * more tiles times blocks of K is refused (HQ_ERR_UNSUPPORTED).  There is no gradient here: the codes
+ * are those of a layer that has been trained.
  */
 hq_status hq_fp8_gemm(const uint8_t* a_codes, const float* a_scales, int64_t M, const uint8_t* w_codes,
                       const float* w_scales, int64_t N, int64_t K, void* Y, int y_dtype, int* dev_status,
@@ -387,7 +391,8 @@ hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int6
  *   order    : int32 [T * top] out: the choice t * top + j of each row, ascending inside an expert;
  *              entries from offsets[E] on are left as they were.
  *   position : int32 [T, top] out: each choice's row, -1 for a dropped one.
- *   workspace: device, 256-byte aligned, at least hq_expert_sort_workspace_bytes(T, top, E) bytes.
+ *   workspace: device, 256-byte aligned, at least hq_expert_sort_workspace_bytes(T, top, E) bytes, not
+ *              shared with a call that may run at the same time (another stream or captured graph).
  *   T >= 0, top >= 1, 1 <= E <= HQ_MAX_EXPERTS, T * top <= 2^30 (HQ_ERR_UNSUPPORTED).
  * hq_expert_dispatch: rows[position[t, j]] = X[t]; X [T, K], rows [T * top, K] in one dtype.  Its
  *   gradient with respect to X is hq_expert_combine of the rows' gradient with weights NULL.

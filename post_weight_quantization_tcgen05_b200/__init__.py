@@ -577,6 +577,13 @@ def hq_debug_fp8_gemm_impl(a_codes, a_scales, offsets, w_codes, w_scales, K: int
                            stream=None) -> None:
     """hq_fp8_gemm (offsets None) or hq_fp8_expert_gemm by a chosen kernel (hq_debug.h)."""
     rows, N = Y.shape
+    lead = () if offsets is None else (w_codes.shape[0],)
+    _want(a_codes, "a_codes", _FP8, (rows, _pitch(K)))
+    _want(a_scales, "a_scales", torch.float32, (_blocks(K), rows))
+    if offsets is not None:
+        _want(offsets, "offsets", torch.int32, (lead[0] + 1,))
+    _want(w_codes, "w_codes", _FP8, (*lead, N, _pitch(K)))
+    _want(w_scales, "w_scales", torch.float32, (*lead, _blocks(N), _blocks(K)))
     _want_status(dev_status)
     a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
     _check(lib.hq_debug_fp8_gemm_impl(a, sa, rows, off, w, sw, 1 if offsets is None else w_codes.shape[0], N, K, y,

@@ -21,11 +21,12 @@
 //            tensor work, more than L2 gives all SMs at once; in a pair each CTA loads its 128 rows
 //            of A and half of the 256 rows of W, 32 KB, and the tensor cores read the other half
 //            from the peer's shared memory.  For many rows.
-//   single : one CTA, a 128 x 128 tile.  For few rows, where the tile's height is mostly padding and
-//            more, smaller tiles keep more SMs at work.
+//   single : one CTA, a 128 x 128 tile.  For some hundred rows, where more, smaller tiles keep more SMs
+//            at work; fewer rows still go to fp8_gemm_few.cu.  Which of them runs is pick_impl's choice.
 //
-// One CTA per SM walks its tiles.  Warp 0 loads the operands by TMA (128 x 128 e4m3 boxes of A and W,
-// 128-byte swizzle, K-major) into a ring of 32 KB stages, one stage per scale block; warp 1 issues
+// One CTA per SM walks its tiles.  Warp 0 loads the operands by TMA (128 rows of A and 128 of W, in a
+// pair 64 for each half of the tile's columns, by 128 columns; 128-byte swizzle, K-major) into a ring of
+// 32 KB stages, one stage per scale block; warp 1 issues
 // the MMAs (in a pair, the even CTA's for both); warp 2 fetches the scales some blocks ahead and
 // leaves their products, and each tile's place, in shared memory; warps 4-11 (two per TMEM lane
 // quadrant, half of the tile's columns each) scale, add and store.  Columns at and past K read as
@@ -36,6 +37,8 @@
 // Every wait is bounded: on expiry the CTA records HQ_ERR_TIMEOUT, waits (bounded) for its
 // in-flight TMA and MMA work, frees TMEM and returns; the CTAs of a pair meet at the end, so that
 // neither leaves while the other may still signal into its shared memory.
+#include <atomic>
+
 #include "fp8_gemm.cuh"
 
 namespace hq {
@@ -454,6 +457,16 @@ hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
   else if (!make_tmap_2d(&map_y, sizeof(TY) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y,
                          static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.rows), p.N * sizeof(TY), 128 / sizeof(TY), 32))
     return HQ_ERR_CUDA;
+  if constexpr (kPair) {
+    // the epilogue's registers come out of those the CTA was launched with: with fewer it would wait for good
+    static std::atomic<int> regs;
+    if (regs.load(std::memory_order_relaxed) == 0) {
+      cudaFuncAttributes attr;
+      HQ_CUDA_TRY(cudaFuncGetAttributes(&attr, fp8_gemm_kernel<kPair, TY>));
+      regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return HQ_ERR_UNSUPPORTED;
+  }
   HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<kPair, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   const int slots = kPair ? kSMs / 2 : kSMs;
   const unsigned grid = static_cast<unsigned>((most < slots ? most : slots) * (kPair ? 2 : 1));

@@ -44,7 +44,9 @@ __device__ __forceinline__ void expert_range(const GemmArgs& a, int e, int& r0, 
   r1 = min(max(a.offsets[e + 1], r0), a.rows);
 }
 
-// All threads: fills start[0 .. E] with tiles of BM rows; valid after the next barrier.
+// All threads: fills start[0 .. E] with tiles of BM rows; valid after the next barrier.  Ranges that do
+// not overlap have rows / BM + E tiles at most; the sums stop there, so that offsets that name rows again
+// and again leave no index outside 32 bits, and no more tiles than the launch allows for.
 template <int BM>
 __device__ __forceinline__ void expert_tiles(const GemmArgs& a, int* start) {
   if (a.offsets == nullptr) {  // one matrix for all rows
@@ -63,16 +65,18 @@ __device__ __forceinline__ void expert_tiles(const GemmArgs& a, int* start) {
   __syncthreads();
   if (threadIdx.x < 32) {
     const int per = (a.E + 31) / 32, e0 = threadIdx.x * per;
+    const int most = a.rows / BM + a.E;
     int sum = 0;
-    for (int e = e0; e < e0 + per && e < a.E; ++e) sum += start[e + 1];
+    for (int e = e0; e < e0 + per && e < a.E; ++e) sum = min(sum + start[e + 1], most);
     int before = sum;
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, before, off);
-      if (static_cast<int>(threadIdx.x) >= off) before += y;
+      if (static_cast<int>(threadIdx.x) >= off) before = min(before + y, most);
     }
-    before -= sum;
+    before = __shfl_up_sync(0xffffffffu, before, 1);  // the lanes before this one
+    if (threadIdx.x == 0) before = 0;
     for (int e = e0; e < e0 + per && e < a.E; ++e) {
-      before += start[e + 1];
+      before = min(before + start[e + 1], most);
       start[e + 1] = before;
     }
   }

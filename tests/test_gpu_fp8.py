@@ -330,6 +330,29 @@ def test_linear_on_a_side_stream_and_in_a_graph(hq, cuda_device, M, N, K):
         assert torch.equal(Y, ref)
 
 
+def test_linears_of_different_kernels_at_once(hq, cuda_device):
+    """Layers of one token, 24, 64, 300 and 2000 rows on streams of their own, over and over: kernels that
+    share the SMs' tensor memory, with clusters and without, give what each gives alone."""
+    N, K = 2048, 1536
+    w, sw = quantise_blocks(hq, activations(2, N, K, "bf16"))
+    sets = []
+    for M in (1, 24, 64, 300, 2000, 1):
+        X = activations(M, M, K, "bf16")
+        ws = hq.alloc_workspace(hq.hq_fp8_linear_workspace_bytes(M, K))
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        hq.hq_fp8_linear(X, w, sw, Y, ws)
+        sets.append((X, ws, Y.clone(), Y.fill_(0), torch.cuda.Stream()))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for X, ws, _, Y, s in sets:
+            hq.hq_fp8_linear(X, w, sw, Y, ws, dev_status=status, stream=s)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for X, _, want, Y, _ in sets:
+        assert torch.equal(Y, want), X.shape
+
+
 # ------------------------------------------------------------------ the kernels one by one
 
 IMPLS = {"single": 1, "pair": 2, "few16": 3, "few64": 4}
@@ -373,6 +396,27 @@ def test_every_kernel_on_experts(hq, cuda_device, sizes, gaps, N, K, impl):
         W = w.view(E, N, -1)[e, :, :K].double() * sw[e, 0].double().repeat_interleave(128)[:K]
         ref[off[e]:off[e + 1]] = A[off[e]:off[e + 1]] @ W.t()
     assert torch.equal(Y.double(), ref)
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("impl", list(IMPLS))
+def test_offsets_whose_ranges_overlap_stay_inside_y(hq, cuda_device, impl):
+    """Device data that a program got wrong: four of the eight experts name all rows.  Every entry of Y is
+    what it was or one of those experts' results, and nothing beside Y is written."""
+    E, rows, N, K = 8, 1500, 132, 128
+    a, sa = small_integers(1, rows, K, 1)
+    w, sw = small_integers(2, E * N, K, N)
+    sw = sw[:, None].expand(E, 2, -1).contiguous()
+    offsets = torch.tensor([0, rows] * 4 + [0], dtype=torch.int32, device="cuda")
+    around = torch.full((rows + 600, N), 0.5, device="cuda")
+    Y = around[300:300 + rows]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hq.hq_debug_fp8_gemm_impl(a, sa.t().contiguous(), offsets, w.view(E, N, -1), sw, K, Y, IMPLS[impl], dev_status=status)
+    A = a[:, :K].double() * sa.double()
+    known = Y == 0.5
+    for e in range(0, E, 2):
+        known |= Y.double() == A @ (w.view(E, N, -1)[e, :, :K].double() * sw[e, 0, 0].double()).t()
+    assert known.all() and (around[:300] == 0.5).all() and (around[300 + rows:] == 0.5).all()
     assert status.item() == 0
 
 
@@ -420,6 +464,28 @@ with torch.cuda.graph(g):
 g.replay(); torch.cuda.synchronize()
 # 1.0 is quantised to 448 with the scale fp32(1 / 448)
 assert (Y - 256).abs().max() < 256 * 2 ** -20 and (y - 256).abs().max() < 256 * 2 ** -20, (Y.max(), y.max())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_a_first_call_of_the_pairs_under_capture(cuda_device):
+    """The same for rows enough that pairs of CTAs run."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, post_weight_quantization_tcgen05_b200 as hq
+torch.cuda.init()
+X = torch.ones((4000, 256), device="cuda"); W = torch.ones((4096, 256), device="cuda"); Y = torch.zeros((4000, 4096), device="cuda")
+w, sw = hq.fp8_blocks_outputs(4096, 256); ws = hq.alloc_workspace(hq.hq_fp8_linear_workspace_bytes(4000, 256))
+torch.cuda.synchronize(); g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    hq.hq_fp8_quantize_blocks(W, w, sw)
+    hq.hq_fp8_linear(X, w, sw, Y, ws)
+g.replay(); torch.cuda.synchronize()
+assert (Y - 256).abs().max() < 256 * 2 ** -20, Y.max()
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
