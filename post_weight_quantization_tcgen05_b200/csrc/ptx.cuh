@@ -74,20 +74,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// The same by polling without a pause, for waits on the critical path: a suspended try_wait returns some
-// hundred cycles after the phase is complete.
-__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          long long limit = kWaitLimitCycles) {
-  const long long start = clock64();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_test(bar, parity)) return true;
-    if (abort != nullptr && *abort) return false;
-    if (clock64() - start > limit) return false;
-  }
-}
-
 // True in one lane of a converged warp; the compiler then knows that a single thread runs what follows.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -282,20 +268,11 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// 4 bytes from global to shared memory without a register between (zeros where !live); the groups of
-// the calling thread complete in order.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
-}
+// 4 bytes of shared memory by their address.
 __device__ __forceinline__ float lds32(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // (d0, d1) += s (v0, v1), both in one instruction

@@ -341,3 +341,95 @@ def test_expert_layer(hq, cuda_device, T, top, E, K, N, dtype):
     blocks = -(-K // 128)
     tol = size * (132 * 2.0 ** -23 + (blocks + 1 + top + 1) * 2.0 ** -24 + HALF_STEP[dtype] * 1.01) + np.abs(ref) * HALF_STEP[dtype]
     assert np.all(np.abs(to_np64(Y) - ref) <= tol)
+
+
+class Layer:
+    """Buffers of an expert layer, forward and backward, in one place: what a graph holds on to."""
+
+    def __init__(self, hq, T, top, E, K, N):
+        self.hq, self.E, self.K = hq, E, K
+        bf16 = dict(dtype=torch.bfloat16, device="cuda")
+        self.X, self.dY = torch.zeros((T, K), **bf16), torch.zeros((T, N), **bf16)
+        self.ids = torch.full((T, top), -1, dtype=torch.int32, device="cuda")
+        self.w = torch.zeros((T, top), device="cuda")
+        self.sorted = hq.expert_sort_outputs(T, top, E)
+        self.ws = hq.alloc_workspace(hq.hq_expert_sort_workspace_bytes(T, top, E))
+        self.codes, self.scales = hq.fp8_rows_outputs(T * top, K)
+        # zeros, as rows that no choice names are left alone
+        self.rows, self.d_rows = torch.zeros((T * top, N), **bf16), torch.zeros((T * top, N), **bf16)
+        self.Y, self.dw = torch.empty((T, N), **bf16), torch.empty((T, top), device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def fill(self, seed, drop):
+        T, top = self.ids.shape
+        self.X.copy_(torch.randn(self.X.shape, generator=gen(seed), device="cuda"))
+        self.dY.copy_(torch.randn(self.dY.shape, generator=gen(seed + 1), device="cuda"))
+        self.w.copy_(torch.rand((T, top), generator=gen(seed + 2), device="cuda"))
+        self.ids.copy_(choices(seed, T, top, self.E, drop))
+
+    def run(self, wc, ws, stream=None):
+        hq, (offsets, order, position) = self.hq, self.sorted
+        hq.hq_expert_sort(self.ids, self.E, offsets, order, position, self.ws, stream=stream)
+        hq.hq_expert_dispatch_fp8(self.X, position, self.codes, self.scales, stream=stream)
+        hq.hq_fp8_expert_gemm(self.codes, self.scales, offsets, wc, ws, self.K, self.rows, self.status, stream=stream)
+        hq.hq_expert_combine(self.rows, position, self.w, self.Y, stream=stream)
+        hq.hq_expert_combine_backward(self.dY, self.rows, position, self.w, self.d_rows, self.dw, stream=stream)
+
+    def results(self):
+        """Y, the weights' gradient, and each choice's row of the rows' gradient (zero if dropped)."""
+        position = self.sorted[2].long()
+        d = self.d_rows[position.clamp(min=0)] * (position >= 0)[..., None]
+        return self.Y.clone(), self.dw.clone(), d
+
+
+@pytest.mark.parametrize("T,top,E,K,N", [(5, 2, 7, 272, 200), (300, 8, 12, 640, 384), (4000, 4, 9, 384, 512)])
+def test_expert_layer_replayed_and_on_two_streams(hq, cuda_device, T, top, E, K, N):
+    W = (torch.randn((E, N, K), generator=gen(3), device="cuda") * 0.05).to(torch.bfloat16)
+    wc, ws = hq.fp8_blocks_outputs(N, K, E)
+    hq.hq_fp8_quantize_blocks(W, wc, ws)
+    layers, drops, want = [Layer(hq, T, top, E, K, N) for _ in range(2)], (0.0, 0.2, 1.0, 0.5), []
+    for seed, drop in enumerate(drops):
+        layers[0].fill(10 * seed, drop)
+        layers[0].run(wc, ws)
+        want.append(layers[0].results())
+    assert not want[2][0].any() and not want[2][1].any()  # all choices dropped: zeros
+    assert want[0][0].any() and want[3][2].any()
+    # captured once, replayed on other tokens and choices
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        layers[0].run(wc, ws)
+    for seed in (1, 2, 0, 3):
+        layers[0].fill(10 * seed, drops[seed])
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(layers[0].results(), want[seed]))
+    # two calls at once, each with buffers of its own
+    streams = [torch.cuda.Stream() for _ in layers]
+    for layer, seed in zip(layers, (0, 1)):
+        layer.fill(10 * seed, drops[seed])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for layer, s in zip(layers, streams):
+            layer.run(wc, ws, stream=s)
+    torch.cuda.synchronize()
+    for layer, seed in zip(layers, (0, 1)):
+        assert all(torch.equal(a, b) for a, b in zip(layer.results(), want[seed]))
+        assert layer.status.item() == 0
+
+
+def test_expert_layer_without_tokens_and_an_expert_named_by_every_choice(hq, cuda_device):
+    from post_weight_quantization_tcgen05_b200 import experts
+    E, K, N, T, top = 3, 256, 128, 5, 4
+    W = (torch.randn((E, N, K), generator=gen(3), device="cuda") * 0.05).to(torch.bfloat16)
+    wc, ws = hq.fp8_blocks_outputs(N, K, E)
+    hq.hq_fp8_quantize_blocks(W, wc, ws)
+    none = torch.empty((0, K), dtype=torch.bfloat16, device="cuda")
+    experts.expert_linear(hq, none, torch.empty((0, top), dtype=torch.int32, device="cuda"), None, wc, ws,
+                          torch.empty((0, N), dtype=torch.bfloat16, device="cuda"))
+    # every choice of every token is the same expert: four equal rows a token, whose sum is exact
+    X = torch.randn((T, K), generator=gen(2), device="cuda").to(torch.bfloat16)
+    Y, one = torch.empty((T, N), dtype=torch.bfloat16, device="cuda"), torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((T, top), 1, dtype=torch.int32, device="cuda")
+    experts.expert_linear(hq, X, ids, None, wc, ws, Y)
+    experts.expert_linear(hq, X, ids[:, :1].contiguous(), None, wc, ws, one)
+    assert one.any() and torch.equal(Y, 4 * one)
