@@ -218,16 +218,20 @@ hq_status launch_expert_sort(const int* ids, int64_t R, int64_t E, int* offsets,
 
 // ---------------------------------------------------------------- rows in vectors
 //
-// The row kernels below give each token a group of 32 .. 256 threads (as many as its row has
-// vectors, in powers of two), and each thread one vector of 16 bytes at a time; rows that are not
-// made of aligned 16-byte vectors are walked element by element by the same code.
+// The row kernels below give each token a group of 32 .. 256 threads (as many as its row has vectors,
+// in powers of two), and each thread a vector of values at a time: 16 bytes that lie together (Vec), or,
+// where rows are not made of aligned 16-byte vectors, four values 32 apart (Loose), so that neighbouring
+// lanes still read neighbouring values.  What bounds those is the loads on their way: with one value a
+// thread 8192 x 8 rows of 5119 bf16 are summed in 500 us, with two in 218, four 202, eight (registers
+// spill) 507; copied in 256, 218, 171, 168 us; the sum's gradient takes 553, 410, 356 us, four of them with
+// two CTAs on an SM (three, which spill: 470 us).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
+  static constexpr bool kSpread = false;
   using Raw = uint4;
-  __device__ __forceinline__ static Raw load(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ static void values(const Raw& a, float (&v)[8]) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -245,13 +249,19 @@ struct Vec<__nv_bfloat16> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const Raw& a) { *reinterpret_cast<uint4*>(p) = a; }
+  // vector i of a row of K values
+  __device__ __forceinline__ static Raw load(const __nv_bfloat16* row, int64_t i, int64_t) {
+    return __ldg(reinterpret_cast<const uint4*>(row) + i);
+  }
+  __device__ __forceinline__ static void store(__nv_bfloat16* row, int64_t i, int64_t, const Raw& a) {
+    *(reinterpret_cast<uint4*>(row) + i) = a;
+  }
 };
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
+  static constexpr bool kSpread = false;
   using Raw = float4;
-  __device__ __forceinline__ static Raw load(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
   __device__ __forceinline__ static void values(const Raw& a, float (&v)[4]) {
     v[0] = a.x;
     v[1] = a.y;
@@ -259,17 +269,50 @@ struct Vec<float> {
     v[3] = a.w;
   }
   __device__ __forceinline__ static Raw pack(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
-  __device__ __forceinline__ static void store(float* p, const Raw& a) { *reinterpret_cast<float4*>(p) = a; }
+  __device__ __forceinline__ static Raw load(const float* row, int64_t i, int64_t) {
+    return __ldg(reinterpret_cast<const float4*>(row) + i);
+  }
+  __device__ __forceinline__ static void store(float* row, int64_t i, int64_t, const Raw& a) {
+    *(reinterpret_cast<float4*>(row) + i) = a;
+  }
 };
 template <typename T>
-struct One {  // one element
-  static constexpr int kN = 1;
-  using Raw = T;
-  __device__ __forceinline__ static Raw load(const T* p) { return *p; }
-  __device__ __forceinline__ static void values(const Raw& a, float (&v)[1]) { v[0] = static_cast<float>(a); }
-  __device__ __forceinline__ static Raw pack(const float (&v)[1]) { return static_cast<T>(v[0]); }
-  __device__ __forceinline__ static void store(T* p, const Raw& a) { *p = a; }
+struct Loose {  // "vector" i: the values i / 32 * 32 kN + i % 32 + 32 u, those of them below K
+  static constexpr int kN = 4;
+  static constexpr bool kSpread = true;
+  struct Raw {
+    T v[kN];
+  };
+  __device__ __forceinline__ static void values(const Raw& a, float (&v)[kN]) {
+#pragma unroll
+    for (int u = 0; u < kN; ++u) v[u] = static_cast<float>(a.v[u]);
+  }
+  __device__ __forceinline__ static Raw pack(const float (&v)[kN]) {
+    Raw a;
+#pragma unroll
+    for (int u = 0; u < kN; ++u) a.v[u] = static_cast<T>(v[u]);
+    return a;
+  }
+  __device__ __forceinline__ static int64_t first(int64_t i) { return (i >> 5) * (32 * kN) + (i & 31); }
+  __device__ __forceinline__ static Raw load(const T* row, int64_t i, int64_t K) {
+    const int64_t at = first(i);
+    Raw a;
+#pragma unroll
+    for (int u = 0; u < kN; ++u) a.v[u] = at + 32 * u < K ? __ldg(row + at + 32 * u) : static_cast<T>(0.f);
+    return a;
+  }
+  __device__ __forceinline__ static void store(T* row, int64_t i, int64_t K, const Raw& a) {
+    const int64_t at = first(i);
+#pragma unroll
+    for (int u = 0; u < kN; ++u)
+      if (at + 32 * u < K) row[at + 32 * u] = a.v[u];
+  }
 };
+// "vectors" of a row of K values
+template <typename V>
+__host__ __device__ __forceinline__ int64_t row_vectors(int64_t K) {
+  return V::kSpread ? (K + 32 * V::kN - 1) / (32 * V::kN) * 32 : K / V::kN;
+}
 
 // Choices handled at once: their positions and weights are in registers, and their rows' loads on
 // their way together.
@@ -305,16 +348,19 @@ template <typename T, template <typename> class V>
 __global__ void __launch_bounds__(kRowThreads)
     expert_dispatch_kernel(const T* __restrict__ X, int64_t tokens, int64_t K, const int* __restrict__ position, int top,
                            int64_t rows, int tpt, T* __restrict__ out) {
-  constexpr int N = V<T>::kN;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
   if (t >= tokens) return;
-  const int64_t vectors = K / N;
+  const int64_t vectors = row_vectors<V<T>>(K);
   const int* pos = position + t * top;
+  Choices c;
+  c.load(pos, nullptr, 0, top, rows);
   for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
-    const typename V<T>::Raw v = V<T>::load(X + t * K + i * N);
-    for (int j = 0; j < top; ++j) {
-      const int p = __ldg(pos + j);
-      if (p >= 0 && p < rows) V<T>::store(out + static_cast<int64_t>(p) * K + i * N, v);
+    const typename V<T>::Raw v = V<T>::load(X + t * K, i, K);
+    for (int j0 = 0; j0 < top; j0 += kChoices) {
+      if (top > kChoices) c.load(pos, nullptr, j0, top, rows);
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j)
+        if (c.p[j] >= 0) V<T>::store(out + static_cast<int64_t>(c.p[j]) * K, i, K, v);
     }
   }
 }
@@ -358,7 +404,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
   constexpr int N = V<T>::kN;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
   if (t >= tokens) return;
-  const int64_t vectors = K / N;
+  const int64_t vectors = row_vectors<V<T>>(K);
   const int* pos = position + t * top;
   const float* wt = weights != nullptr ? weights + t * top : nullptr;
   Choices c;
@@ -372,7 +418,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
       typename V<T>::Raw raw[kChoices];
 #pragma unroll
       for (int j = 0; j < kChoices; ++j)
-        if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K + i * N);
+        if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K, i, K);
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) {
         if (c.p[j] < 0) continue;
@@ -382,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
         for (int k = 0; k < N; ++k) acc[k] = fmaf(c.w[j], z[k], acc[k]);
       }
     }
-    V<T>::store(Y + t * K + i * N, V<T>::pack(acc));
+    V<T>::store(Y + t * K, i, K, V<T>::pack(acc));
   }
 }
 
@@ -391,7 +437,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
 // in registers; a token's threads add them up in a fixed order.  Bound by DRAM, half reads and half
 // writes: 8192 x 8 rows of 5120 bf16 228 us, 6.25 TB/s.
 template <typename T, template <typename> class V>
-__global__ void __launch_bounds__(kRowThreads, 3)
+__global__ void __launch_bounds__(kRowThreads, V<T>::kSpread ? 2 : 3)
     expert_combine_backward_kernel(const T* __restrict__ dY, const T* __restrict__ rows, int64_t nrows, int64_t K,
                                    const int* __restrict__ position, const float* __restrict__ weights, int64_t tokens,
                                    int top, int tpt, T* __restrict__ d_rows, float* __restrict__ d_weights) {
@@ -400,17 +446,17 @@ __global__ void __launch_bounds__(kRowThreads, 3)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
   const bool live = t < tokens;  // all threads stay for the barriers
-  const int64_t vectors = live ? K / N : 0;
+  const int64_t vectors = live ? row_vectors<V<T>>(K) : 0;
   for (int j0 = 0; j0 < top; j0 += kChoices) {
     Choices c;
     c.load(position + t * top, weights + t * top, j0, live ? top : 0, nrows);
     float dot[kChoices] = {};
     for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
       typename V<T>::Raw raw[kChoices];
-      const typename V<T>::Raw raw_g = V<T>::load(dY + t * K + i * N);
+      const typename V<T>::Raw raw_g = V<T>::load(dY + t * K, i, K);
 #pragma unroll
       for (int j = 0; j < kChoices; ++j)
-        if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K + i * N);
+        if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K, i, K);
       float g[N];
       V<T>::values(raw_g, g);
 #pragma unroll
@@ -423,7 +469,7 @@ __global__ void __launch_bounds__(kRowThreads, 3)
           dot[j] = fmaf(g[k], z[k], dot[j]);
           d[k] = c.w[j] * g[k];
         }
-        V<T>::store(d_rows + static_cast<int64_t>(c.p[j]) * K + i * N, V<T>::pack(d));
+        V<T>::store(d_rows + static_cast<int64_t>(c.p[j]) * K, i, K, V<T>::pack(d));
       }
     }
 #pragma unroll
@@ -464,7 +510,7 @@ static RowGrid row_grid(int64_t tokens, int64_t vectors) {
 template <typename T, template <typename> class V>
 static void dispatch_as(const void* X, int64_t tokens, int64_t K, const int* position, int64_t top, void* out,
                         cudaStream_t s) {
-  const RowGrid g = row_grid(tokens, K / V<T>::kN);
+  const RowGrid g = row_grid(tokens, row_vectors<V<T>>(K));
   expert_dispatch_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(static_cast<const T*>(X), tokens, K, position,
                                                               static_cast<int>(top), tokens * top, g.tpt,
                                                               static_cast<T*>(out));
@@ -476,7 +522,7 @@ static void dispatch_typed(const void* X, int64_t tokens, int64_t K, const int* 
   if (rows_vec(K * sizeof(T), X, out))
     dispatch_as<T, Vec>(X, tokens, K, position, top, out, s);
   else
-    dispatch_as<T, One>(X, tokens, K, position, top, out, s);
+    dispatch_as<T, Loose>(X, tokens, K, position, top, out, s);
 }
 
 hq_status launch_expert_dispatch(const void* X, int x_dtype, int64_t tokens, int64_t K, const int* position, int64_t top,
@@ -507,7 +553,7 @@ hq_status launch_expert_dispatch_fp8(const void* X, int x_dtype, int64_t tokens,
 template <typename T, template <typename> class V>
 static void combine_as(const void* rows, int64_t K, const int* position, const float* weights, int64_t tokens,
                        int64_t top, void* Y, cudaStream_t s) {
-  const RowGrid g = row_grid(tokens, K / V<T>::kN);
+  const RowGrid g = row_grid(tokens, row_vectors<V<T>>(K));
   expert_combine_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(static_cast<const T*>(rows), tokens * top, K, position,
                                                              weights, tokens, static_cast<int>(top), g.tpt,
                                                              static_cast<T*>(Y));
@@ -519,7 +565,7 @@ static void combine_typed(const void* rows, int64_t K, const int* position, cons
   if (rows_vec(K * sizeof(T), rows, Y))
     combine_as<T, Vec>(rows, K, position, weights, tokens, top, Y, s);
   else
-    combine_as<T, One>(rows, K, position, weights, tokens, top, Y, s);
+    combine_as<T, Loose>(rows, K, position, weights, tokens, top, Y, s);
 }
 
 hq_status launch_expert_combine(const void* rows, int dtype, int64_t tokens, int64_t K, const int* position, int64_t top,
@@ -535,7 +581,7 @@ hq_status launch_expert_combine(const void* rows, int dtype, int64_t tokens, int
 template <typename T, template <typename> class V>
 static void combine_backward_as(const void* dY, const void* rows, int64_t K, const int* position, const float* weights,
                                 int64_t tokens, int64_t top, void* d_rows, float* d_weights, cudaStream_t s) {
-  const RowGrid g = row_grid(tokens, K / V<T>::kN);
+  const RowGrid g = row_grid(tokens, row_vectors<V<T>>(K));
   expert_combine_backward_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(
       static_cast<const T*>(dY), static_cast<const T*>(rows), tokens * top, K, position, weights, tokens,
       static_cast<int>(top), g.tpt, static_cast<T*>(d_rows), d_weights);
@@ -548,7 +594,7 @@ static void combine_backward_typed(const void* dY, const void* rows, int64_t K, 
   if (rows_vec(K * sizeof(T), dY, rows, d_rows))
     combine_backward_as<T, Vec>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
   else
-    combine_backward_as<T, One>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
+    combine_backward_as<T, Loose>(dY, rows, K, position, weights, tokens, top, d_rows, d_weights, s);
 }
 
 hq_status launch_expert_combine_backward(const void* dY, const void* rows, int dtype, int64_t tokens, int64_t K,

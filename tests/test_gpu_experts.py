@@ -239,6 +239,16 @@ def test_rows_that_are_not_16_byte_aligned(hq, cuda_device, offset):
     assert (out[0][1] - out[1][1]).abs().max() <= K * 2.0 ** -23 * 16 * K  # sums of K terms in another order
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 31, 32, 33, 127, 129, 255, 257, 1023, 1025, 2050])
+def test_rows_of_odd_widths(hq, cuda_device, K, dtype):
+    """Widths around what a warp takes of a row that is not made of 16-byte vectors, more choices than are
+    handled at once."""
+    test_dispatch(hq, cuda_device, 19, 9, 4, K, dtype)
+    test_combine(hq, cuda_device, 19, 9, 4, K, dtype, True)
+    test_combine_backward(hq, cuda_device, 19, 9, 4, K, dtype)
+
+
 def test_positions_out_of_range_count_as_dropped(hq, cuda_device):
     """Device data that a program got wrong is not followed out of the rows."""
     T, top, K = 4, 2, 64
