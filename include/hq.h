@@ -408,7 +408,7 @@ hq_status hq_fp8_expert_gemm(const uint8_t* a_codes, const float* a_scales, int6
  *   counts as dropped.  Rows that no choice names are neither read nor written (whatever they or a
  *   dropped choice's weight hold).  Outputs must not alias inputs.  K >= 1, K <= 2^24.
  * Device pointers, asynchronous, identical run to run.  Rows made of 16-byte aligned vectors take
- * 16-byte accesses, others element accesses with the same results (d_weights: up to fp32 rounding).
+ * 16-byte accesses, others accesses by the element with the same results (d_weights: up to fp32 rounding).
  */
 size_t hq_expert_sort_workspace_bytes(int64_t T, int64_t top, int64_t E);
 hq_status hq_expert_sort(const int32_t* ids, int64_t T, int64_t top, int64_t E, int32_t* offsets, int32_t* order,

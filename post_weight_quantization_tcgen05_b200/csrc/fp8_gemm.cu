@@ -22,7 +22,7 @@
 //            of A and half of the 256 rows of W, 32 KB, and the tensor cores read the other half
 //            from the peer's shared memory.  For many rows.
 //   single : one CTA, a 128 x 128 tile.  For some hundred rows, where more, smaller tiles keep more SMs
-//            at work; fewer rows still go to fp8_gemm_few.cu.  Which of them runs is pick_impl's choice.
+//            at work; few rows, and few tiles, go to fp8_gemm_few.cu.  Which of them runs is pick_impl's choice.
 //
 // One CTA per SM walks its tiles.  Warp 0 loads the operands by TMA (128 rows of A and 128 of W, in a
 // pair 64 for each half of the tile's columns, by 128 columns; 128-byte swizzle, K-major) into a ring of
@@ -37,6 +37,7 @@
 // Every wait is bounded: on expiry the CTA records HQ_ERR_TIMEOUT, waits (bounded) for its
 // in-flight TMA and MMA work, frees TMEM and returns; the CTAs of a pair meet at the end, so that
 // neither leaves while the other may still signal into its shared memory.
+#include <algorithm>
 #include <atomic>
 
 #include "fp8_gemm.cuh"
@@ -488,29 +489,44 @@ hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
 
 namespace {
 
-// Few rows: the kernel that reads the weights once, in tiles of 16 rows up to 32 rows (1 x 5120 x 5120:
-// 9 us against 18 us of the single CTAs; 24 x 17408 x 5120: 20.1 us against 23.5 us with tiles of 64, the
-// second tile's weights coming from L2) and of 64 up to 64 where the single CTAs' tiles would leave half
-// the SMs idle (64 x 5120 x 5120: 14.8 us against 18.2 us, 64 x 5120 x 17408: 25 us against 50 us; not
-// 64 x 17408 x 5120: 27 us against 21 us).  Experts go by their average, as their sizes differ: tiles of 16
-// up to 24 rows (800 rows, 48 experts 2560 x 5120: 100 us against 109 us with tiles of 64; 2048 rows, 64
-// experts 164 us against 153 us), of 64 up to 48 (2048 rows: 153 us against 167 us of the single CTAs;
-// 4096 218 us against 194 us).  More rows: whichever of the other two has less to do, by its rounds of
-// tiles over the SMs.  A block of 128 columns takes a single CTA 0.32 us, a pair (four times the work)
-// 0.47 us, and a launch 5 or 6 us around them: 384 x 5120 x 5120 18 us against 24 us, 768 31 us against
-// 25 us, 1024 43 us either way, 2048 69 us against 61 us, 256 x 17408 x 5120 34 us against 26 us.
+// Up to 32 rows: the kernel that reads the weights once, in tiles of 16 (1 x 5120 x 5120: 9 us against
+// 18 us of the single CTAs; 24 x 17408 x 5120: 20.1 us against 23.5 us with tiles of 64, the second tile's
+// weights coming from L2).  Experts go by their average, as their sizes differ: tiles of 16 up to 24 rows
+// (800 rows, 48 experts 2560 x 5120: 100 us against 109 us with tiles of 64; 2048 rows, 64 experts 164 us
+// against 153 us), of 64 up to 48 (2048 rows: 153 us against 167 us of the single CTAs; 4096 218 us against
+// 194 us).
+// Else by what each would take, in units of 10 ns from timings.  A block of 128 columns takes a single CTA
+// 0.32 us, a pair (four times the work) 0.47 us, in rounds of tiles over the SMs, and a launch 5 or 6 us
+// around them: 384 x 5120 x 5120 18 us against 24 us, 768 31 us against 25 us, 1024 43 us either way, 2048
+// 69 us against 61 us, 256 x 17408 x 5120 34 us against 26 us.  Those two do not split K, so few tiles leave
+// SMs idle; the kernel for few rows does, and then takes as long as its loads, or as one CTA its part:
+// 300 x 256 x 17408 14 and 15 us in tiles of 16 and 64 against 44 us of the single CTAs, 128 x 512 x 5120
+// 9.2 and 9.3 us against 17 us, 256 x 1024 x 5120 14 and 13 us against 17 us, 64 x 5120 x 17408 25 us with
+// 64 against 50 us; but 96 x 5120 x 5120 19 and 20 us against 17 us, 64 x 17408 x 5120 27 us with 64
+// against 21 us.
 int pick_impl(const Fp8Gemm& p) {
   const bool experts = p.offsets != nullptr;
   const int64_t each = ceil_div(p.rows, p.E);
   if (each <= (experts ? 24 : 32)) return kFp8Few16;
-  if (experts ? each <= 48 : each <= 64 && ceil_div(p.N, 128) * 2 <= fp8::kSMs) return kFp8Few64;
+  if (experts && each <= 48) return kFp8Few64;
   // an expert's last tile is half full on average
   const int64_t m128 = experts ? p.rows / 128 + ceil_div(p.E, 2) : ceil_div(p.rows, 128);
   const int64_t m256 = experts ? p.rows / 256 + ceil_div(p.E, 2) : ceil_div(p.rows, 256);
-  const int64_t blocks = ceil_div(p.K, kFp8Block);
-  const int64_t single = 500 + 32 * blocks * ceil_div(m128 * ceil_div(p.N, 128), fp8::kSMs);
+  const int64_t blocks = ceil_div(p.K, kFp8Block), n128 = ceil_div(p.N, 128);
+  const int64_t single = 500 + 32 * blocks * ceil_div(m128 * n128, fp8::kSMs);
   const int64_t pair = 600 + 47 * blocks * ceil_div(m256 * ceil_div(p.N, 256), fp8::kSMs / 2);
-  return pair < single ? kFp8Pair : kFp8Single;
+  int64_t best = std::min(single, pair);
+  int impl = pair < single ? kFp8Pair : kFp8Single;
+  if (experts) return impl;
+  const auto few = [&](int64_t rows, int64_t launch, int64_t block, int64_t per_thousand) {
+    const int64_t tiles = ceil_div(p.rows, rows) * n128;
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>(8, 2 * fp8::kSMs / tiles));
+    return launch + std::max(block * ceil_div(blocks, split), tiles * blocks * per_thousand / 1000);
+  };
+  const int64_t few16 = few(16, 600, 27, 165), few64 = few(64, 700, 45, 360);
+  if (few16 < best) best = few16, impl = kFp8Few16;
+  if (few64 < best) impl = kFp8Few64;
+  return impl;
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
-// The e4m3 product for few rows (a serving step): bound by reading the weights.  The mathematics and
-// the scaling after every block of 128 columns are those of fp8_gemm.cu, with the operands exchanged:
-// 128 rows of W are the MMA's 128 rows, BT rows of A (16 or 64) its columns.  A block's accumulator is
+// The e4m3 product for few rows (a serving step), bound by reading the weights, and for few tiles.  The
+// mathematics and the scaling after every block of 128 columns are those of fp8_gemm.cu, with the operands
+// exchanged: 128 rows of W are the MMA's 128 rows, BT rows of A (16 or 64) its columns.  A block's accumulator is
 // then BT columns of tensor memory, so 256 of them hold 16 or 4 accumulators and the hand-over to the
 // epilogue, several hundred cycles, never holds up the loads; a stage takes 16 KB of W and 2 or 8 KB
 // of A, and two CTAs on an SM keep 10 stages on their way.

@@ -330,6 +330,22 @@ def test_linear_on_a_side_stream_and_in_a_graph(hq, cuda_device, M, N, K):
         assert torch.equal(Y, ref)
 
 
+@pytest.mark.parametrize("M,N,K", [(294, 256, 6043), (130, 100, 2000), (700, 300, 4096), (40, 4000, 700), (512, 1024, 640)])
+def test_few_tiles_of_many_rows(hq, cuda_device, M, N, K):
+    """More rows than a serving step but few tiles: K is split, and the layer is the product of the
+    quantised rows bit for bit."""
+    X, W = activations(1, M, K, "bf16"), activations(2, N, K, "bf16") * 0.02
+    w, sw = quantise_blocks(hq, W)
+    a, sa = quantise_rows(hq, X)
+    Y, Z = (torch.full((M, N), float("nan"), device="cuda") for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hq.hq_fp8_gemm(a, sa, w, sw, K, Y, dev_status=status)
+    hq.hq_fp8_linear(X, w, sw, Z, hq.alloc_workspace(hq.hq_fp8_linear_workspace_bytes(M, K)), dev_status=status)
+    assert torch.equal(Y, Z) and status.item() == 0
+    ref, size = oracle.fp8_product(*oracle.fp8_quantize(to_np64(X), 1), *oracle.fp8_quantize(to_np64(W), 128))
+    check_product(Y, ref, size, K)
+
+
 def test_linears_of_different_kernels_at_once(hq, cuda_device):
     """Layers of one token, 24, 64, 300 and 2000 rows on streams of their own, over and over: kernels that
     share the SMs' tensor memory, with clusters and without, give what each gives alone."""
