@@ -315,15 +315,15 @@ __host__ __device__ __forceinline__ int64_t row_vectors(int64_t K) {
 }
 
 // Choices handled at once: their positions and weights are in registers, and their rows' loads on
-// their way together.
-constexpr int kChoices = 8;
-
+// their way together.  C is 4 where a token has no more, else 8: fewer registers, more CTAs on an SM
+// (8192 x 4 rows of 5120 bf16 102 -> 72 us, their gradient 153 -> 121 us, one row a token 85 -> 50 us).
+template <int C>
 struct Choices {
-  int p[kChoices];  // -1: dropped, or none
-  float w[kChoices];
+  int p[C];  // -1: dropped, or none
+  float w[C];
   __device__ __forceinline__ void load(const int* position, const float* weights, int j0, int top, int64_t rows) {
 #pragma unroll
-    for (int j = 0; j < kChoices; ++j) {
+    for (int j = 0; j < C; ++j) {
       p[j] = j0 + j < top ? __ldg(position + j0 + j) : -1;
       if (p[j] >= rows) p[j] = -1;
       if (p[j] < 0) p[j] = -1;
@@ -352,14 +352,15 @@ __global__ void __launch_bounds__(kRowThreads)
   if (t >= tokens) return;
   const int64_t vectors = row_vectors<V<T>>(K);
   const int* pos = position + t * top;
-  Choices c;
+  constexpr int C = 8;
+  Choices<C> c;
   c.load(pos, nullptr, 0, top, rows);
   for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
     const typename V<T>::Raw v = V<T>::load(X + t * K, i, K);
-    for (int j0 = 0; j0 < top; j0 += kChoices) {
-      if (top > kChoices) c.load(pos, nullptr, j0, top, rows);
+    for (int j0 = 0; j0 < top; j0 += C) {
+      if (top > C) c.load(pos, nullptr, j0, top, rows);
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j)
+      for (int j = 0; j < C; ++j)
         if (c.p[j] >= 0) V<T>::store(out + static_cast<int64_t>(c.p[j]) * K, i, K, v);
     }
   }
@@ -397,8 +398,8 @@ __global__ void __launch_bounds__(256)
 
 // Y[t] = sum_j w[t, j] rows[position[t, j]] in the order of j, summed in fp32 and rounded once.  Bound by
 // reading the rows, eight of them on their way in every thread: 8192 x 8 of 5120 bf16 128 us, 5.9 TB/s.
-template <typename T, template <typename> class V>
-__global__ void __launch_bounds__(kRowThreads, 3)
+template <typename T, template <typename> class V, int C>
+__global__ void __launch_bounds__(kRowThreads, C == 8 ? 3 : V<T>::kSpread ? 4 : 5)
     expert_combine_kernel(const T* __restrict__ rows, int64_t nrows, int64_t K, const int* __restrict__ position,
                           const float* __restrict__ weights, int64_t tokens, int top, int tpt, T* __restrict__ Y) {
   constexpr int N = V<T>::kN;
@@ -407,20 +408,20 @@ __global__ void __launch_bounds__(kRowThreads, 3)
   const int64_t vectors = row_vectors<V<T>>(K);
   const int* pos = position + t * top;
   const float* wt = weights != nullptr ? weights + t * top : nullptr;
-  Choices c;
+  Choices<C> c;
   c.load(pos, wt, 0, top, nrows);
   for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
     float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
-    for (int j0 = 0; j0 < top; j0 += kChoices) {
-      if (top > kChoices) c.load(pos, wt, j0, top, nrows);
-      typename V<T>::Raw raw[kChoices];
+    for (int j0 = 0; j0 < top; j0 += C) {
+      if (top > C) c.load(pos, wt, j0, top, nrows);
+      typename V<T>::Raw raw[C];
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j)
+      for (int j = 0; j < C; ++j)
         if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K, i, K);
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) {
+      for (int j = 0; j < C; ++j) {
         if (c.p[j] < 0) continue;
         float z[N];
         V<T>::values(raw[j], z);
@@ -436,31 +437,31 @@ __global__ void __launch_bounds__(kRowThreads, 3)
 // p = position[t, j]; a dropped choice has d_weights 0.  Eight choices at a time, their dot products
 // in registers; a token's threads add them up in a fixed order.  Bound by DRAM, half reads and half
 // writes: 8192 x 8 rows of 5120 bf16 228 us, 6.25 TB/s.
-template <typename T, template <typename> class V>
-__global__ void __launch_bounds__(kRowThreads, V<T>::kSpread ? 2 : 3)
+template <typename T, template <typename> class V, int C>
+__global__ void __launch_bounds__(kRowThreads, C == 4 ? 4 : V<T>::kSpread ? 2 : 3)
     expert_combine_backward_kernel(const T* __restrict__ dY, const T* __restrict__ rows, int64_t nrows, int64_t K,
                                    const int* __restrict__ position, const float* __restrict__ weights, int64_t tokens,
                                    int top, int tpt, T* __restrict__ d_rows, float* __restrict__ d_weights) {
   constexpr int N = V<T>::kN;
-  __shared__ float part[kRowThreads / 32][kChoices];
+  __shared__ float part[kRowThreads / 32][C];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRowThreads / tpt) + threadIdx.x / tpt;
   const bool live = t < tokens;  // all threads stay for the barriers
   const int64_t vectors = live ? row_vectors<V<T>>(K) : 0;
-  for (int j0 = 0; j0 < top; j0 += kChoices) {
-    Choices c;
+  for (int j0 = 0; j0 < top; j0 += C) {
+    Choices<C> c;
     c.load(position + t * top, weights + t * top, j0, live ? top : 0, nrows);
-    float dot[kChoices] = {};
+    float dot[C] = {};
     for (int64_t i = threadIdx.x % tpt; i < vectors; i += tpt) {
-      typename V<T>::Raw raw[kChoices];
+      typename V<T>::Raw raw[C];
       const typename V<T>::Raw raw_g = V<T>::load(dY + t * K, i, K);
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j)
+      for (int j = 0; j < C; ++j)
         if (c.p[j] >= 0) raw[j] = V<T>::load(rows + static_cast<int64_t>(c.p[j]) * K, i, K);
       float g[N];
       V<T>::values(raw_g, g);
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) {
+      for (int j = 0; j < C; ++j) {
         if (c.p[j] < 0) continue;
         float z[N], d[N];
         V<T>::values(raw[j], z);
@@ -473,17 +474,17 @@ __global__ void __launch_bounds__(kRowThreads, V<T>::kSpread ? 2 : 3)
       }
     }
 #pragma unroll
-    for (int j = 0; j < kChoices; ++j) {
+    for (int j = 0; j < C; ++j) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], off);
     }
     if (lane == 0) {
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) part[warp][j] = dot[j];
+      for (int j = 0; j < C; ++j) part[warp][j] = dot[j];
     }
     __syncthreads();
     const int j = threadIdx.x % tpt;
-    if (live && j < kChoices && j0 + j < top) {
+    if (live && j < C && j0 + j < top) {
       float sum = 0.f;
       for (int k = 0; k < tpt / 32; ++k) sum += part[warp + k][j];
       d_weights[t * top + j0 + j] = sum;
@@ -554,7 +555,8 @@ template <typename T, template <typename> class V>
 static void combine_as(const void* rows, int64_t K, const int* position, const float* weights, int64_t tokens,
                        int64_t top, void* Y, cudaStream_t s) {
   const RowGrid g = row_grid(tokens, row_vectors<V<T>>(K));
-  expert_combine_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(static_cast<const T*>(rows), tokens * top, K, position,
+  const auto kernel = top <= 4 ? expert_combine_kernel<T, V, 4> : expert_combine_kernel<T, V, 8>;
+  kernel<<<g.ctas, kRowThreads, 0, s>>>(static_cast<const T*>(rows), tokens * top, K, position,
                                                              weights, tokens, static_cast<int>(top), g.tpt,
                                                              static_cast<T*>(Y));
 }
@@ -582,7 +584,8 @@ template <typename T, template <typename> class V>
 static void combine_backward_as(const void* dY, const void* rows, int64_t K, const int* position, const float* weights,
                                 int64_t tokens, int64_t top, void* d_rows, float* d_weights, cudaStream_t s) {
   const RowGrid g = row_grid(tokens, row_vectors<V<T>>(K));
-  expert_combine_backward_kernel<T, V><<<g.ctas, kRowThreads, 0, s>>>(
+  const auto kernel = top <= 4 ? expert_combine_backward_kernel<T, V, 4> : expert_combine_backward_kernel<T, V, 8>;
+  kernel<<<g.ctas, kRowThreads, 0, s>>>(
       static_cast<const T*>(dY), static_cast<const T*>(rows), tokens * top, K, position, weights, tokens,
       static_cast<int>(top), g.tpt, static_cast<T*>(d_rows), d_weights);
 }
