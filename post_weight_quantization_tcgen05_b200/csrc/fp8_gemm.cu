@@ -13,7 +13,9 @@
 // and SM at 128 bytes a cycle); a signal from the MMAs to the epilogue or back takes about 400 cycles,
 // reading an accumulator 400.  With two whole accumulators that came to 1040 cycles (645 us); handed over
 // by halves of 128 columns the two halves' hand-overs overlap each other's MMAs, which then read A's
-// operand twice: 607 us, 2.4 PFLOP/s.
+// operand twice: 605 us, 2.4 PFLOP/s (525 us on constant operands, which take less power: 860 cycles a
+// block).  What is left over the MMAs: the warps of the epilogue that share a quarter of the SM with a
+// warp of another role take some 300 cycles a block longer, and the stores of a tile 2000 cycles.
 //
 // Two tilings of one kernel:
 //   pair   : two CTAs (a cluster) compute a 256 x 256 tile with cta_group::2 MMAs, each of them 128
@@ -27,8 +29,8 @@
 // One CTA per SM walks its tiles.  Warp 0 loads the operands by TMA (128 rows of A and 128 of W, in a
 // pair 64 for each half of the tile's columns, by 128 columns; 128-byte swizzle, K-major) into a ring of
 // 32 KB stages, one stage per scale block; warp 1 issues
-// the MMAs (in a pair, the even CTA's for both); warp 2 fetches the scales some blocks ahead and
-// leaves their products, and each tile's place, in shared memory; warps 4-11 (two per TMEM lane
+// the MMAs (in a pair, the even CTA's for both); warps 2 and 3 fetch the scales some blocks ahead and
+// leave their products, and each tile's place, in shared memory; warps 4-11 (two per TMEM lane
 // quadrant, half of the tile's columns each) scale, add and store.  Columns at and past K read as
 // zeros (the tensor map's extent is K, not the row pitch), as do rows past the operands' ends.  A
 // tile of an expert that ends inside it computes rows of the next expert as well (against the wrong
@@ -99,65 +101,79 @@ __device__ __forceinline__ uint4 pack16(const float* v, __nv_bfloat16) {
 
 // A warp's 32 rows x NC columns of Y, one row of sums a lane, through shared memory of its own in
 // pieces of 32 rows x 128 bytes: a lane's own row would go out as 16-byte pieces of 32 different lines
-// (measured 10,000 cycles for a 128 x 256 tile, the time of eleven blocks of the product).  A whole
-// piece leaves by a TMA store, which runs on while the warp takes up the next tile; one that an
-// expert's last row cuts, or unaligned rows of Y, by stores of the lanes, 8 a row.  16-byte part p of
-// row r is kept at place p ^ (r % 8), the 128-byte swizzle of the tensor map.  Rows from `rows_left`
-// on and columns from N on are not written.
+// (measured 10,000 cycles for a 128 x 256 tile, the time of eleven blocks of the product; this way 2,000).
+// Whole pieces leave by TMA stores, two at a time, which run on while the warp takes up the next tile; one
+// that an expert's last row cuts, or unaligned rows of Y, by stores of the lanes, 8 a row.  16-byte part p
+// of row r is kept at place p ^ (r % 8), the 128-byte swizzle of the tensor map.  Rows from `rows_left`
+// on and columns from N on are not written.  The elected lane is always the same: it waits for its own
+// stores.
 template <int NC, typename TY>
 __device__ __forceinline__ void store_rows(const GemmArgs& a, const CUtensorMap* map, uint8_t* stage, int row, int col,
-                                           int rows_left, const float (&acc)[NC], int lane, int& turn) {
+                                           int rows_left, const float (&acc)[NC], int lane) {
   constexpr int kPer = 16 / sizeof(TY);  // columns of 16 bytes
   constexpr int kPiece = 8 * kPer;       // columns of a piece
   constexpr int kPieces = NC / kPiece;
+  constexpr int kAtOnce = kPieces < 2 ? kPieces : 2;
+  static_assert(kPieces % kAtOnce == 0 && kAtOnce * 32 * 128 <= kStoreBytes, "pieces of a turn");
   if (rows_left <= 0 || col >= a.N) return;
   const bool whole = a.y_aligned && rows_left >= 32;
   (void)HQ_IN_BOUNDS(row >= 0 && row + min(rows_left, 32) <= a.rows);
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < kPieces; i += kAtOnce) {
+      // the pieces before, which lay here, have been read by their stores
+      if (ptx::elect_one()) ptx::bulk_wait_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          *reinterpret_cast<uint4*>(stage + u * (32 * 128) + lane * 128 + ((p ^ (lane & 7)) << 4)) =
+              pack16(acc + (i + u) * kPiece + p * kPer, TY());
+      ptx::fence_async_smem();
+      __syncwarp();
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u)
+          if (col + (i + u) * kPiece < a.N) ptx::tma_store_2d(map, stage + u * (32 * 128), col + (i + u) * kPiece, row);
+        ptx::bulk_commit();
+      }
+    }
+    return;
+  }
+  if (ptx::elect_one()) ptx::bulk_wait_read<0>();
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = i * kPiece;
-    uint8_t* buf = stage + (turn++ & 1) * (32 * 128);  // two pieces take turns, across tiles too
-    // the piece before the last, which lay here, has been read by its store
-    if (lane == 0) ptx::bulk_wait_read<1>();
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < 8; ++p)
-      *reinterpret_cast<uint4*>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = pack16(acc + c + p * kPer, TY());
-    if (whole) {
-      ptx::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (col + c < a.N) ptx::tma_store_2d(map, buf, col + c, row);
-        ptx::bulk_commit();
-      }
+      *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = pack16(acc + c + p * kPer, TY());
+    __syncwarp();
+    TY* out = static_cast<TY*>(a.Y) + static_cast<int64_t>(row) * a.N;
+    if (a.y_aligned) {
+      const int p = lane & 7;
+      const int at = col + c + p * kPer;
+      if (at < a.N)  // whole 16 bytes, as the rows are made of them
+        for (int r = lane >> 3; r < rows_left && r < 32; r += 4)
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * a.N + at) =
+              *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
     } else {
-      __syncwarp();
-      TY* out = static_cast<TY*>(a.Y) + static_cast<int64_t>(row) * a.N;
-      if (a.y_aligned) {
-        const int p = lane & 7;
-        const int at = col + c + p * kPer;
-        if (at < a.N)  // whole 16 bytes, as the rows are made of them
-          for (int r = lane >> 3; r < rows_left; r += 4)
-            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * a.N + at) =
-                *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) << 4));
-      } else {
-        // 4 bytes a lane, a row at a time
-        constexpr int kEach = 4 / sizeof(TY);
-        const int at = col + c + lane * kEach;
-        for (int r = 0; r < rows_left && r < 32; ++r) {
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-          TY* o = out + static_cast<int64_t>(r) * a.N + at;
-          if (at + kEach <= a.N && (reinterpret_cast<uintptr_t>(o) & 3) == 0) {
-            *reinterpret_cast<uint32_t*>(o) = v;
-          } else {
-            const TY* e = reinterpret_cast<const TY*>(&v);
+      // 4 bytes a lane, a row at a time
+      constexpr int kEach = 4 / sizeof(TY);
+      const int at = col + c + lane * kEach;
+      for (int r = 0; r < rows_left && r < 32; ++r) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        TY* o = out + static_cast<int64_t>(r) * a.N + at;
+        if (at + kEach <= a.N && (reinterpret_cast<uintptr_t>(o) & 3) == 0) {
+          *reinterpret_cast<uint32_t*>(o) = v;
+        } else {
+          const TY* e = reinterpret_cast<const TY*>(&v);
 #pragma unroll
-            for (int k = 0; k < kEach; ++k)
-              if (at + k < a.N) o[k] = e[k];
-          }
+          for (int k = 0; k < kEach; ++k)
+            if (at + k < a.N) o[k] = e[k];
         }
       }
-      if (lane == 0) ptx::bulk_commit();  // an empty group in the store's place
     }
   }
 }
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sh.acce[b >> 1][b & 1], kEpiWarps);  // of a pair: half the warps of two CTAs
     }
     for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(&sh.scf[s], 1);
+      ptx::mbar_init(&sh.scf[s], 2);
       ptx::mbar_init(&sh.sce[s], kEpiWarps);
     }
     ptx::mbar_init(&sh.drain, 1);
@@ -313,11 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mma_commit(&sh.drain);
       ptx::mbar_wait(&sh.drain, 0, nullptr);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------ scales
-    // A lane fetches the scales of 4 rows, kFetch blocks ahead of the block it writes.
+    // Each warp has 64 of the rows; a lane fetches the scales of 2, kFetch blocks ahead of the block it
+    // writes.  (One warp for all rows 1 % slower: it holds up the epilogue warps that it shares the issue
+    // slots of a quarter of the SM with.)
     pdl_wait();
-    float sa[kFetch][4], sw[kFetch][2];
+    const int r0 = (warp - 2) * 64 + lane;
+    float sa[kFetch][2], sw[kFetch][2];
     Tile x{};
     int k = args.kblocks, i = -1;  // the block to fetch: the first of the tile after tile i
     auto fetch = [&](int f, int g) {
@@ -327,12 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++i;
         x = tile_at<kBM, kBN>(args, sh.start, first + i * step);
         // its place is read by the epilogue after its first block's scales are announced, later
-        if (lane == 0) sh.places[i % kPlaces] = x;
+        if (threadIdx.x == 64) sh.places[i % kPlaces] = x;
       }
       const float* col = args.a_scales + static_cast<int64_t>(k) * args.rows;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = x.m0 + rank * kRows + r * 32 + lane;
+      for (int r = 0; r < 2; ++r) {
+        const int row = x.m0 + rank * kRows + r0 + r * 32;
         sa[f][r] = row < x.m1 ? __ldg(col + row) : 0.f;
       }
 #pragma unroll
@@ -359,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sh.scales[(g0 + f) % kScales][h][r * 32 + lane] = sa[f][r] * sw[f][h];
+          for (int r = 0; r < 2; ++r) sh.scales[(g0 + f) % kScales][h][r0 + r * 32] = sa[f][r] * sw[f][h];
         fetch(f, g0 + f + kFetch);
       }
       __syncwarp();
@@ -381,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sce = ptx::smem_u32(&sh.sce[0]);
     const uint32_t scale_at = ptx::smem_u32(&sh.scales[0][h][q * 32 + lane]);
     bool ok = true, seen = false;  // seen: the block's accumulator has been seen filled
-    int g = 0, turn = 0;
+    int g = 0;
     for (int i = 0; i < own && ok; ++i) {
       float acc[NC];
 #pragma unroll
@@ -427,9 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Tile x = sh.places[i % kPlaces];
       const int row = x.m0 + rank * kRows + q * 32;
-      store_rows<NC, TY>(args, &mapY, stage, row, x.n0 + h * NC, x.m1 - row, acc, lane, turn);
+      store_rows<NC, TY>(args, &mapY, stage, row, x.n0 + h * NC, x.m1 - row, acc, lane);
     }
-    if (lane == 0) ptx::bulk_wait<0>();
+    if (ptx::elect_one()) ptx::bulk_wait<0>();
     if (!ok) fail();
   }
 
