@@ -17,7 +17,7 @@
 // dependent, with the first weights loaded meanwhile: for 16 rows of 5120 11.0 us against 13.2 us.
 //
 // On the device, weights from DRAM: 1 x 5120 x 5120 9 us (set-up 0.8 us, 3 us to the first weights, the
-// cluster's sums 1.2 us), 1 x 17408 x 5120 18.5 us (4.8 TB/s), 24 x 17408 x 5120 20 us (4.5 TB/s); experts,
+// cluster's sums 1.2 us), 1 x 17408 x 5120 18.5 us (4.8 TB/s), 24 x 17408 x 5120 19 us (4.8 TB/s); experts,
 // 512 rows of 48 2560 x 5120, 87 us (7.2 TB/s, nearly all of it reads).
 //
 // Per CTA: warp 0 loads, warp 1 issues the MMAs, warp 2 leaves the products of the scales in shared
