@@ -537,10 +537,11 @@ int pick_impl(const Fp8Gemm& p) {
   int64_t best = std::min(single, pair);
   int impl = pair < single ? kFp8Pair : kFp8Single;
   if (experts) return impl;
-  const auto few = [&](int64_t rows, int64_t launch, int64_t block, int64_t per_thousand) {
+  const auto few = [&](int64_t rows, int64_t launch, int64_t block, double per_thousand) {
     const int64_t tiles = ceil_div(p.rows, rows) * n128;
     const int64_t split = std::max<int64_t>(1, std::min<int64_t>(8, 2 * fp8::kSMs / tiles));
-    return launch + std::max(block * ceil_div(blocks, split), tiles * blocks * per_thousand / 1000);
+    const int64_t loads = static_cast<int64_t>(1e-3 * per_thousand * tiles * blocks);  // any size: no overflow
+    return launch + std::max(block * ceil_div(blocks, split), loads);
   };
   const int64_t few16 = few(16, 600, 27, 165), few64 = few(64, 700, 45, 360);
   if (few16 < best) best = few16, impl = kFp8Few16;
