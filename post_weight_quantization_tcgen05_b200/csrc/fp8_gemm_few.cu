@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     }
     if (!ok) fail();
     if (split > 1) {
+      // both meetings are of whole warps, which columns at and past N have split by the second
+      __syncwarp();
       ptx::cluster_sync();  // every part is in its CTA's shared memory
       if (ok && own > 0) {
         const Tile x = sh.places[0];
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
           }
         }
       }
+      __syncwarp();
       ptx::cluster_sync_relaxed();  // no CTA leaves while another reads its part
     }
   }

@@ -1,0 +1,30 @@
+"""Rules of the e4m3 product's kernels that a wrong run would show only by luck, read off their source."""
+
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "post_weight_quantization_tcgen05_b200", "csrc")
+PRODUCTS = ("fp8_gemm.cu", "fp8_gemm_few.cu")
+
+
+def code(name):
+    """A source file without its comments."""
+    return re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+
+
+def test_every_cluster_barrier_is_reached_by_whole_warps():
+    """The cluster barriers are .aligned: all lanes of a warp execute them together.  So the statement
+    before one is a barrier that brings the warp together, of the warp, the CTA or the cluster."""
+    whole = re.compile(r"(?:__syncwarp|__syncthreads|ptx::cluster_sync(?:_relaxed)?)\(\)$")
+    found = 0
+    for name in PRODUCTS:
+        before = ""
+        for statement in re.split(r"[;{}]", code(name)):
+            statement = re.sub(r"^if constexpr \(\w+\) ", "", " ".join(statement.split()))
+            if re.fullmatch(r"ptx::cluster_sync(?:_relaxed)?\(\)", statement):
+                found += 1
+                assert whole.search(before), f"{name}: {statement} after '{before}'"
+            if statement:
+                before = statement
+    assert found == 6
