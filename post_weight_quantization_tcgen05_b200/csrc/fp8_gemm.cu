@@ -348,11 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // its place is read by the epilogue after its first block's scales are announced, later
         if (threadIdx.x == 64) sh.places[i % kPlaces] = x;
       }
+      // not __ldg: the kernel that writes these scales may have run beside this one until pdl_wait
       const float* col = args.a_scales + static_cast<int64_t>(k) * args.rows;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = x.m0 + rank * kRows + r0 + r * 32;
-        sa[f][r] = row < x.m1 ? __ldg(col + row) : 0.f;
+        sa[f][r] = row < x.m1 ? __ldcg(col + row) : 0.f;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

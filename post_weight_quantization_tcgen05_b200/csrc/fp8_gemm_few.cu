@@ -258,11 +258,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
         // its place is read by the epilogue after its first block's scales are announced, later
         if (lane == 0) sh.places[i % kPlaces] = x;
       }
+      // not __ldg: the kernel that writes these scales may have run beside this one until pdl_wait
       const float* col = args.a_scales + static_cast<int64_t>(k0 + k) * args.rows;
 #pragma unroll
       for (int r = 0; r < kPer; ++r) {
         const int row = x.m0 + r * 32 + lane;
-        sa[f][r] = row < x.m1 ? __ldg(col + row) : 0.f;
+        sa[f][r] = row < x.m1 ? __ldcg(col + row) : 0.f;
       }
       sw[f] = __ldg(args.w_scales + (static_cast<int64_t>(x.e) * args.nblocks + x.n0 / kFp8Block) * args.kblocks + k0 + k);
       ++k;

@@ -28,3 +28,16 @@ def test_every_cluster_barrier_is_reached_by_whole_warps():
             if statement:
                 before = statement
     assert found == 6
+
+
+def test_scales_of_a_running_quantiser_are_not_read_as_constants():
+    """hq_fp8_linear launches the product while the kernel that writes the activations' scales still runs.
+    ld.global.nc (__ldg) is for data that nothing writes while the kernel runs, so no such load may take
+    an address made from a_scales; the weights' scales are constants."""
+    for name in PRODUCTS:
+        src = code(name)
+        made = {"a_scales"} | set(re.findall(r"(\w+)\s*=\s*[^;=]*\ba_scales\b", src))
+        loads = re.findall(r"(\w+)\(([^()]*(?:\([^()]*\)[^()]*)*)\)", src)
+        constant = [arg for f, arg in loads if f == "__ldg" and made & set(re.findall(r"\w+", arg))]
+        assert not constant, f"{name}: __ldg({constant[0]})"
+        assert any(f == "__ldcg" and made & set(re.findall(r"\w+", arg)) for f, arg in loads), name

@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from test_gpu_fp8 import IMPLS, TYPES, hq, small_integers  # noqa: F401
+from test_gpu_fp8 import IMPLS, TYPES, activations, hq, quantise_blocks, quantise_rows, small_integers  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -24,4 +24,25 @@ def test_clusters_whose_last_columns_split_a_warp(hq, cuda_device, M, N, K, impl
         for y in Y:
             hq.hq_debug_fp8_gemm_impl(a, sa, None, w, sw, K, y, IMPLS[impl], dev_status=status)
         assert (Y == ref.float().to(TYPES[dt])).all()
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 640, 1024), (5, 384, 5120), (24, 2000, 1537), (100, 2048, 640), (700, 5000, 300),
+                                   (3000, 2600, 1024)])
+def test_layers_that_take_turns_in_one_workspace(hq, cuda_device, M, N, K):  # noqa: F811
+    """Activations 2^12 apart in size, one after the other through the same workspace without a wait, a
+    product starting while its rows are still quantised: each result is that of the two steps apart."""
+    w, sw = quantise_blocks(hq, activations(1, N, K, "bf16"))
+    ws = hq.alloc_workspace(hq.hq_fp8_linear_workspace_bytes(M, K))
+    X = [activations(2 + i, M, K, "bf16") * 2.0 ** (12 * i - 6) for i in range(2)]
+    want = [torch.empty((M, N), device="cuda") for _ in X]
+    for x, y in zip(X, want):
+        hq.hq_fp8_gemm(*quantise_rows(hq, x), w, sw, K, y)
+    Y = torch.full((40, M, N), float("nan"), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for i, y in enumerate(Y):
+        hq.hq_fp8_linear(X[i % 2], w, sw, y, ws, dev_status=status)
+    for i in range(2):
+        assert (Y[i::2] == want[i]).all(), i
     assert status.item() == 0
