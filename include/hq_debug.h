@@ -51,6 +51,27 @@ hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, 
                                  void* Y, int y_dtype, int* dev_status, int impl, hq_stream_t stream);
 
 /*
+ * The failure path of the e4m3 products' bounded waits, made to run on purpose: hq_debug_fp8_gemm_impl
+ * with
+ *   wait_limit_cycles : 1e5 .. 4e9, the SM cycles any pipeline wait may take before the CTA records
+ *                       HQ_ERR_TIMEOUT in *dev_status and stops (with less, a call could give up while
+ *                       its first loads are still on their way);
+ *   withhold_stage    : -1 (an ordinary call), or 0 .. 3: the MMA issuer never releases that stage of
+ *                       the operand ring after its first use, so the wait to refill it expires in
+ *                       every CTA whose blocks of 128 columns come round to it (a ring has 4 stages, 5
+ *                       in tiles of 16 rows).  Where a cluster shares a tile's K only its first CTA
+ *                       does so; the others finish their parts and meet it.  The stream and context
+ *                       stay usable; Y is undefined.
+ *   dev_status        : device int, required (zeroed by the caller).
+ * Y is fp32 (HQ_ERR_UNSUPPORTED for HQ_BF16): variants of the kernels of their own take the two arguments,
+ * so that ordinary calls do not pay for them.
+ */
+hq_status hq_debug_fp8_gemm_timeout(const uint8_t* a_codes, const float* a_scales, int64_t rows,
+                                    const int32_t* offsets, const uint8_t* w_codes, const float* w_scales, int64_t E,
+                                    int64_t N, int64_t K, void* Y, int y_dtype, int* dev_status, int impl,
+                                    int64_t wait_limit_cycles, int withhold_stage, hq_stream_t stream);
+
+/*
  * The failure path of the tensor-core SYRK's bounded waits, made to run on purpose (no
  * counterpart on the pages; the library's rule that a device-side wait never hangs).  The
  * tcgen05 SYRK of hq_hessian_accumulate on bf16 X with

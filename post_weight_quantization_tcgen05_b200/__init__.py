@@ -90,6 +90,8 @@ _SIGS = {
     "hq_fp8_linear": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _i64, _vp, _int, _vp, _sz, _vp, _vp]),
     "hq_fp8_expert_gemm": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _vp]),
     "hq_debug_fp8_gemm_impl": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _int, _vp]),
+    "hq_debug_fp8_gemm_timeout": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp, _int, _i64, _int,
+                                         _vp]),
     "hq_expert_sort_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "hq_expert_sort": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
     "hq_expert_dispatch": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp]),
@@ -573,9 +575,7 @@ def hq_fp8_expert_gemm(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y,
            "hq_fp8_expert_gemm")
 
 
-def hq_debug_fp8_gemm_impl(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y, impl: int, dev_status=None,
-                           stream=None) -> None:
-    """hq_fp8_gemm (offsets None) or hq_fp8_expert_gemm by a chosen kernel (hq_debug.h)."""
+def _debug_fp8_gemm(name: str, a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y, dev_status, stream, *last) -> None:
     rows, N = Y.shape
     lead = () if offsets is None else (w_codes.shape[0],)
     _want(a_codes, "a_codes", _FP8, (rows, _pitch(K)))
@@ -586,8 +586,23 @@ def hq_debug_fp8_gemm_impl(a_codes, a_scales, offsets, w_codes, w_scales, K: int
     _want(w_scales, "w_scales", torch.float32, (*lead, _blocks(N), _blocks(K)))
     _want_status(dev_status)
     a, sa, off, w, sw, y, st = _ptrs(a_codes, a_scales, offsets, w_codes, w_scales, Y, dev_status)
-    _check(lib.hq_debug_fp8_gemm_impl(a, sa, rows, off, w, sw, 1 if offsets is None else w_codes.shape[0], N, K, y,
-                                      _dtype(Y), st, int(impl), _stream(stream)), "hq_debug_fp8_gemm_impl")
+    _check(getattr(lib, name)(a, sa, rows, off, w, sw, 1 if offsets is None else w_codes.shape[0], N, K, y, _dtype(Y), st,
+                              *last, _stream(stream)), name)
+
+
+def hq_debug_fp8_gemm_impl(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y, impl: int, dev_status=None,
+                           stream=None) -> None:
+    """hq_fp8_gemm (offsets None) or hq_fp8_expert_gemm by a chosen kernel (hq_debug.h)."""
+    _debug_fp8_gemm("hq_debug_fp8_gemm_impl", a_codes, a_scales, offsets, w_codes, w_scales, K, Y, dev_status, stream,
+                    int(impl))
+
+
+def hq_debug_fp8_gemm_timeout(a_codes, a_scales, offsets, w_codes, w_scales, K: int, Y, impl: int, dev_status,
+                              wait_limit_cycles: int, withhold_stage: int = -1, stream=None) -> None:
+    """The same with a runtime wait limit and, for the test of its timeout path, one operand stage that
+    the MMA issuer never releases (hq_debug.h)."""
+    _debug_fp8_gemm("hq_debug_fp8_gemm_timeout", a_codes, a_scales, offsets, w_codes, w_scales, K, Y, dev_status, stream,
+                    int(impl), int(wait_limit_cycles), int(withhold_stage))
 
 
 def hq_expert_sort_workspace_bytes(T: int, top: int, E: int) -> int:

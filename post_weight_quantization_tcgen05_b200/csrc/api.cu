@@ -94,6 +94,14 @@ hq_status check_fp8_gemm(const Fp8Gemm& g) {
   return HQ_OK;
 }
 
+// A product by a chosen kernel.
+hq_status debug_fp8_gemm(const Fp8Gemm& g, int impl, cudaStream_t s) {
+  const hq_status st = check_fp8_gemm(g);
+  if (st != HQ_OK || g.rows == 0) return st;
+  if (impl < kFp8Auto || impl > kFp8Few64 || (g.offsets == nullptr && g.E != 1)) return HQ_ERR_INVALID;
+  return launch_fp8_gemm(g, impl, s);
+}
+
 size_t fp8_linear_scales_offset(int64_t M, int64_t K) { return round_up(static_cast<size_t>(M) * fp8_pitch(K), 256); }
 size_t fp8_linear_workspace(int64_t M, int64_t K) {
   return fp8_linear_scales_offset(M, K) + round_up(static_cast<size_t>(M) * ceil_div(K, 128) * sizeof(float), 256);
@@ -555,10 +563,20 @@ hq_status hq_debug_fp8_gemm_impl(const uint8_t* a_codes, const float* a_scales, 
                                  const uint8_t* w_codes, const float* w_scales, int64_t E, int64_t N, int64_t K,
                                  void* Y, int y_dtype, int* dev_status, int impl, hq_stream_t stream) {
   const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status, nullptr, 0, false};
-  const hq_status st = check_fp8_gemm(g);
-  if (st != HQ_OK || rows == 0) return st;
-  if (impl < kFp8Auto || impl > kFp8Few64 || (offsets == nullptr && E != 1)) return HQ_ERR_INVALID;
-  return launch_fp8_gemm(g, impl, static_cast<cudaStream_t>(stream));
+  return debug_fp8_gemm(g, impl, static_cast<cudaStream_t>(stream));
+}
+
+hq_status hq_debug_fp8_gemm_timeout(const uint8_t* a_codes, const float* a_scales, int64_t rows,
+                                    const int32_t* offsets, const uint8_t* w_codes, const float* w_scales, int64_t E,
+                                    int64_t N, int64_t K, void* Y, int y_dtype, int* dev_status, int impl,
+                                    int64_t wait_limit_cycles, int withhold_stage, hq_stream_t stream) {
+  if (y_dtype == HQ_BF16) return HQ_ERR_UNSUPPORTED;
+  if (dev_status == nullptr || wait_limit_cycles < 100000 || wait_limit_cycles > kWaitLimitCycles ||
+      withhold_stage < -1 || withhold_stage > 3)
+    return HQ_ERR_INVALID;
+  const Fp8Gemm g{a_codes, a_scales, rows, offsets, w_codes, w_scales, E, N, K, Y, y_dtype, dev_status, nullptr, 0, false,
+                  true, wait_limit_cycles, withhold_stage};
+  return debug_fp8_gemm(g, impl, static_cast<cudaStream_t>(stream));
 }
 
 size_t hq_expert_sort_workspace_bytes(int64_t T, int64_t top, int64_t E) {

@@ -178,7 +178,7 @@ __device__ __forceinline__ void store_rows(const GemmArgs& a, const CUtensorMap*
   }
 }
 
-template <bool kPair, typename TY>
+template <bool kPair, typename TY, bool kTimeout>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW,
                     const __grid_constant__ CUtensorMap mapY, GemmArgs args) {
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* stores = smem + kStages * kStageBytes;
   Shared& sh = *reinterpret_cast<Shared*>(stores + kEpiWarps * kStoreBytes);
   volatile int* abort_flag = &sh.abort;
+  const long long limit = wait_limit<kTimeout>(args);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (void)HQ_IN_BOUNDS(x.m0 < args.rows && x.n0 < args.N);
       for (int k = 0; k < args.kblocks; ++k, ++g) {
         const int s = g % kStages;
-        if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
+        if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag, limit)) {
           ok = false;
           break;
         }
@@ -288,13 +289,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int g = 0; g < blocks && ok; ++g) {
       const int s = g % kStages, b = g & 1;
-      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag)) {
+      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag, limit)) {
         ok = false;
         break;
       }
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        if (g >= 2 && !ptx::mbar_wait(&sh.acce[b][h], ((g >> 1) - 1) & 1, abort_flag)) {
+        if (g >= 2 && !ptx::mbar_wait(&sh.acce[b][h], ((g >> 1) - 1) & 1, abort_flag, limit)) {
           ok = false;
           break;
         }
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mma_commit(&sh.accf[b][h]);
       }
       if (!ok) break;
+      if (kTimeout && g == args.withhold_stage) continue;
       if constexpr (kPair)
         ptx::mma_commit_pair(&sh.empty[s]);
       else
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int g0 = 0; g0 < blocks; g0 += kScaleHalf) {
       const int half = (g0 / kScaleHalf) & 1;
       if (g0 >= kScales) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[half], ((g0 / kScales) - 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[half], ((g0 / kScales) - 1) & 1, abort_flag, limit));
         if (!ok) break;
       }
 #pragma unroll
@@ -410,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = g & 1;
         // the warp goes on or gives up as one: a wait may run out for some of its lanes only
         if (g % kScaleHalf == 0) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag, limit));
           if (!ok) break;
         }
         if (!__all_sync(0xffffffffu, seen)) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.accf[b][half], (g >> 1) & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.accf[b][half], (g >> 1) & 1, abort_flag, limit));
           if (!ok) break;
         }
         ptx::tc_fence_after();
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kPair, typename TY>
+template <bool kPair, typename TY, bool kTimeout = false>
 hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
   constexpr int kTile = kPair ? 256 : 128;
   const int64_t most = most_tiles(p, kTile, kTile);
@@ -483,15 +485,15 @@ hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
     static std::atomic<int> regs;
     if (regs.load(std::memory_order_relaxed) == 0) {
       cudaFuncAttributes attr;
-      HQ_CUDA_TRY(cudaFuncGetAttributes(&attr, fp8_gemm_kernel<kPair, TY>));
+      HQ_CUDA_TRY(cudaFuncGetAttributes(&attr, fp8_gemm_kernel<kPair, TY, kTimeout>));
       regs.store(attr.numRegs, std::memory_order_relaxed);
     }
     if (regs.load(std::memory_order_relaxed) < kRegsLaunch) return HQ_ERR_UNSUPPORTED;
   }
-  HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<kPair, TY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  HQ_CUDA_TRY(cudaFuncSetAttribute(fp8_gemm_kernel<kPair, TY, kTimeout>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   const int slots = kPair ? kSMs / 2 : kSMs;
   const unsigned grid = static_cast<unsigned>((most < slots ? most : slots) * (kPair ? 2 : 1));
-  HQ_LAUNCH_CHAINED(launch_product(p, fp8_gemm_kernel<kPair, TY>, grid, kThreads, kSmem, kPair ? 2 : 1, s, map_a, map_w,
+  HQ_LAUNCH_CHAINED(launch_product(p, fp8_gemm_kernel<kPair, TY, kTimeout>, grid, kThreads, kSmem, kPair ? 2 : 1, s, map_a, map_w,
                                    map_y, a));
   return HQ_OK;
 }
@@ -499,9 +501,11 @@ hq_status run_gemm(const Fp8Gemm& p, cudaStream_t s) {
 }  // namespace
 
 hq_status gemm_single(const Fp8Gemm& p, cudaStream_t s) {
+  if (p.timeout) return run_gemm<false, float, true>(p, s);
   return p.y_dtype == HQ_F32 ? run_gemm<false, float>(p, s) : run_gemm<false, __nv_bfloat16>(p, s);
 }
 hq_status gemm_pair(const Fp8Gemm& p, cudaStream_t s) {
+  if (p.timeout) return run_gemm<true, float, true>(p, s);
   return p.y_dtype == HQ_F32 ? run_gemm<true, float>(p, s) : run_gemm<true, __nv_bfloat16>(p, s);
 }
 

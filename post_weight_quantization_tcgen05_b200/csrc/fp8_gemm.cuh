@@ -30,6 +30,10 @@ struct GemmArgs {
   int E;
   int y_aligned;          // rows of Y are 16-byte aligned (its tensor map is valid)
   int* status;
+  // read by the kernels' kTimeout variants only, which run the test of the timeout path (as arguments
+  // of every call they cost 0.1 to 0.2 us: 384 x 5120 x 5120 17.67 -> 17.87 us)
+  long long wait_limit;  // cycles a pipeline wait may take before the CTA gives up
+  int withhold_stage;    // -1, or a ring stage whose first release the MMA issuer skips
 };
 
 // An expert's rows.  Offsets are device data: a range outside [0, rows] is cut to it and an inverted
@@ -42,6 +46,11 @@ __device__ __forceinline__ void expert_range(const GemmArgs& a, int e, int& r0, 
   }
   r0 = min(max(a.offsets[e], 0), a.rows);
   r1 = min(max(a.offsets[e + 1], r0), a.rows);
+}
+
+template <bool kTimeout>
+__device__ __forceinline__ long long wait_limit(const GemmArgs& a) {
+  return kTimeout ? a.wait_limit : kWaitLimitCycles;
 }
 
 // All threads: fills start[0 .. E] with tiles of BM rows; valid after the next barrier.  Ranges that do
@@ -135,6 +144,8 @@ inline hq_status gemm_args(const Fp8Gemm& p, int64_t tiles, uint32_t box_a, uint
   a.E = static_cast<int>(p.E);
   a.y_aligned = aligned(p.Y, 16) && p.N * (p.y_dtype == HQ_F32 ? 4 : 2) % 16 == 0;
   a.status = p.status;
+  a.wait_limit = p.wait_limit;
+  a.withhold_stage = p.withhold_stage;
   if (!make_tmap_2d(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a_codes, static_cast<uint64_t>(p.K),
                     static_cast<uint64_t>(p.rows), pitch, kBK, box_a) ||
       !make_tmap_2d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w_codes, static_cast<uint64_t>(p.K),

@@ -80,7 +80,7 @@ struct Few {
 // grid: CTAs in clusters of `split`; cluster c takes tiles c, c + clusters, ...  TX: uint8_t (A's codes
 // and scales are read), or the type of the activations X, which are quantised here; then BT == 16, there
 // is a tile for every cluster, and a CTA's part of K has at most kPanel blocks.
-template <int BT, typename TY, typename TX>
+template <int BT, typename TY, typename TX, bool kTimeout>
 __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW,
                         GemmArgs args, int split, const TX* __restrict__ X) {
@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
   uint8_t* panel = smem + kStages * kStageBytes;  // A's codes, if quantised here: 2 KB a block
   Shared<BT, kQuantise>& sh = *reinterpret_cast<Shared<BT, kQuantise>*>(panel + F::kPanelBytes);
   volatile int* abort_flag = &sh.abort;
+  const long long limit = wait_limit<kTimeout>(args);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
       for (int k = 0; k < kn; ++k, ++g) {
         const int s = g % kStages;
         if (kQuantise && g < kStages) continue;  // on its way
-        if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag)) {
+        if (g >= kStages && !ptx::mbar_wait(&sh.empty[s], ((g / kStages) - 1) & 1, abort_flag, limit)) {
           ok = false;
           break;
         }
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     constexpr uint32_t kIdesc = ptx::idesc(ptx::kFmtE4M3, kRows, BT, false, false);
     for (int g = 0; g < blocks; ++g) {
       const int s = g % kStages, b = g % kAccs;
-      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag) ||
-          (g >= kAccs && !ptx::mbar_wait(&sh.acce[b], ((g / kAccs) - 1) & 1, abort_flag))) {
+      if (!ptx::mbar_wait(&sh.full[s], (g / kStages) & 1, abort_flag, limit) ||
+          (g >= kAccs && !ptx::mbar_wait(&sh.acce[b], ((g / kAccs) - 1) & 1, abort_flag, limit))) {
         ok = false;
         break;
       }
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
         ptx::mma_f8(dacc, ptx::sdesc_sw128(sw + kk * 32, 16, 1024), ptx::sdesc_sw128(sa + kk * 32, 16, 1024), kIdesc,
                     kk > 0 ? 1u : 0u);
       ptx::mma_commit(&sh.accf[b]);
-      ptx::mma_commit(&sh.empty[s]);
+      if (!kTimeout || g != args.withhold_stage || rank != 0) ptx::mma_commit(&sh.empty[s]);
     }
     if (!ok) {
       fail();
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
     for (int g0 = 0; g0 < blocks; g0 += kScaleHalf) {
       const int half = (g0 / kScaleHalf) & 1;
       if (g0 >= kScales) {
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[half], ((g0 / kScales) - 1) & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.sce[half], ((g0 / kScales) - 1) & 1, abort_flag, limit));
         if (!ok) break;
       }
 #pragma unroll
@@ -313,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM)
         // the warp goes on or gives up as one: a wait may run out for some of its lanes only
         ok = __all_sync(0xffffffffu,
                         (kQuantise || g % kScaleHalf != 0 ||
-                         ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag)) &&
-                            ptx::mbar_wait(&sh.accf[b], (g / kAccs) & 1, abort_flag));
+                         ptx::mbar_wait(&sh.scf[(g / kScaleHalf) & 1], (g / kScales) & 1, abort_flag, limit)) &&
+                            ptx::mbar_wait(&sh.accf[b], (g / kAccs) & 1, abort_flag, limit));
         if (!ok) break;
         ptx::tc_fence_after();
         const float4* scale = reinterpret_cast<const float4*>(sh.scales[kQuantise ? g : g % kScales]);
@@ -411,7 +412,7 @@ int clusters_at_once(int split) {
   static std::atomic<int> known[kMaxSplit + 1];
   int n = known[split].load(std::memory_order_relaxed);
   if (n > 0) return n;
-  const auto kernel = fp8_gemm_few_kernel<BT, __nv_bfloat16, TX>;
+  const auto kernel = fp8_gemm_few_kernel<BT, __nv_bfloat16, TX, false>;
   constexpr int kSmem = Few<BT, BT == 16>::kSmem;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(split));
@@ -446,7 +447,7 @@ int pick_split(const Fp8Gemm& p) {
   return 1;
 }
 
-template <int BT, typename TY, typename TX>
+template <int BT, typename TY, typename TX, bool kTimeout = false>
 hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
   const int64_t most = most_tiles(p, BT, kRows);
   CUtensorMap map_a, map_w;
@@ -454,7 +455,7 @@ hq_status run_few(const Fp8Gemm& p, cudaStream_t s) {
   const hq_status st = gemm_args(p, most, BT, kRows, a, map_a, map_w);
   if (st != HQ_OK) return st;
   constexpr int kSmem = Few<BT, !std::is_same<TX, uint8_t>::value>::kSmem;
-  const auto kernel = fp8_gemm_few_kernel<BT, TY, TX>;
+  const auto kernel = fp8_gemm_few_kernel<BT, TY, TX, kTimeout>;
   HQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   const int split = pick_split<BT>(p);
   const int64_t clusters = split > 1 ? ceil_div(p.rows, BT) * ceil_div(p.N, kRows) : std::min<int64_t>(most, kSlots);
@@ -479,6 +480,7 @@ bool few_quantises(const Fp8Gemm& p) {
 }
 
 hq_status gemm_few(const Fp8Gemm& p, int tile_rows, cudaStream_t s) {
+  if (p.timeout) return tile_rows == 64 ? run_few<64, float, uint8_t, true>(p, s) : run_few<16, float, uint8_t, true>(p, s);
   return p.y_dtype == HQ_F32 ? run_few_as<float>(p, tile_rows, s) : run_few_as<__nv_bfloat16>(p, tile_rows, s);
 }
 

@@ -220,6 +220,11 @@ struct Fp8Gemm {
   const void* X;
   int x_dtype;
   bool chained;
+  // the test of the timeout path (fp32 Y), with the limit and the stage as for launch_syrk_tc; of a
+  // cluster only the first CTA's issuer keeps the stage
+  bool timeout = false;
+  long long wait_limit = kWaitLimitCycles;
+  int withhold_stage = -1;
 };
 enum Fp8Impl { kFp8Auto = 0, kFp8Single = 1, kFp8Pair = 2, kFp8Few16 = 3, kFp8Few64 = 4 };
 hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s);
