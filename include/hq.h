@@ -330,8 +330,9 @@ hq_status hq_hessian_unpack_bf16tril(const uint8_t* in, int64_t K, float* H_full
  * hq_fp8_quantize_blocks: E weights W [E, N, K] (w_dtype) -> codes [E, N, pitch], scales
  *   [E, ceil(N / 128), ceil(K / 128)].  E >= 1 (1 for one layer, the number of experts otherwise).
  * K >= 1, N >= 1; K <= 2^24, E * N < 2^31 (N <= 2^22), E <= HQ_MAX_EXPERTS, M <= 2^30
- * (HQ_ERR_UNSUPPORTED).  Any alignment of X and W that their type allows; 16-byte aligned rows take
- * 16-byte loads, others element loads with the same results.  Asynchronous; identical run to run.
+ * (HQ_ERR_UNSUPPORTED).  Any alignment of X and W that their type allows: rows that do not start at
+ * 16-byte boundaries are read in the aligned 16-byte pieces that hold them (their values at the edges of
+ * the matrix one by one), with the same results.  Asynchronous; identical run to run.
  */
 #define HQ_MAX_EXPERTS 1024
 int64_t hq_fp8_pitch(int64_t K); /* 0 for K < 1 */
@@ -347,9 +348,8 @@ hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t 
  * y_dtype (HQ_BF16 or HQ_F32).  Y [rows, N], row-major.
  * hq_fp8_gemm: one weight for all M rows.  M >= 0 (M == 0 is a no-op).
  * hq_fp8_linear: the same from activations X [M, K] in x_dtype, quantised on the way (into the
- *   workspace, or, for few rows, by the product's own kernel): the result of hq_fp8_quantize_rows followed by
- *   hq_fp8_gemm, bit for bit.  workspace: device,
- *   256-byte aligned, at least hq_fp8_linear_workspace_bytes(M, K) bytes (HQ_ERR_WORKSPACE), not
+ *   workspace, or, for up to four rows, by the product's own kernel): the result of
+ *   hq_fp8_quantize_rows followed by hq_fp8_gemm, bit for bit.  workspace: device, 256-byte aligned, at least hq_fp8_linear_workspace_bytes(M, K) bytes (HQ_ERR_WORKSPACE), not
  *   shared with a call that may run at the same time (another stream, or another captured graph);
  *   NULL is accepted where that size is 0.
  * hq_fp8_expert_gemm: rows offsets[e] .. offsets[e + 1] - 1 of A and Y meet weight e of W

@@ -37,13 +37,18 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
-// Programmatic dependent launch along the factorisation's chain of short kernels (the small fp64
-// products, their split-K reduce, the leaves): a kernel launched by launch_chained may be
-// scheduled while its predecessor on the stream still runs.  It calls pdl_wait before touching
-// memory (it returns once the predecessor has completed and its writes are visible), and
-// pdl_launch_dependents near its end, so that its own successor is scheduled in turn without
-// holding SM slots for long (slots the second stream's work would otherwise use).  In a kernel
-// launched the ordinary way both are no-ops.
+// Programmatic dependent launch: a kernel launched by launch_chained may be scheduled while its
+// predecessor on the stream still runs, once all CTAs of that one have called pdl_launch_dependents.
+// pdl_wait returns once the predecessor has completed and its writes are visible.  Before it a kernel
+// writes nothing and reads only what was written before its predecessor started (where that one was
+// launched the ordinary way: by anything before it on the stream).  What the predecessor writes is never
+// read by __ldg (ld.global.nc), which is for data that nothing writes while the kernel runs.
+// Along the factorisation's chain of short kernels (the small fp64 products, their split-K reduce, the
+// leaves) every kernel is chained to the next: it calls pdl_wait before touching memory, and
+// pdl_launch_dependents near its end, so that its successor is scheduled in turn without holding SM
+// slots for long (slots the second stream's work would otherwise use).  The e4m3 product behind its
+// quantiser, and the second half of the experts' sort, are the only links of theirs: the first kernel
+// lets the second start at once.  In a kernel launched the ordinary way both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

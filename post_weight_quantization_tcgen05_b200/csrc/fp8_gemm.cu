@@ -13,9 +13,12 @@
 // and SM at 128 bytes a cycle); a signal from the MMAs to the epilogue or back takes about 400 cycles,
 // reading an accumulator 400.  With two whole accumulators that came to 1040 cycles (645 us); handed over
 // by halves of 128 columns the two halves' hand-overs overlap each other's MMAs, which then read A's
-// operand twice: 605 us, 2.4 PFLOP/s (525 us on constant operands, which take less power: 860 cycles a
-// block).  What is left over the MMAs: the warps of the epilogue that share a quarter of the SM with a
-// warp of another role take some 300 cycles a block longer, and the stores of a tile 2000 cycles.
+// operand twice: 605 to 634 us on a rested GPU, 2.3 to 2.4 PFLOP/s.  Under load the power limit lowers the
+// clock: after two seconds of such calls 748 us at 1372 MHz (median of 61 samples), and 513 us at 1957 MHz
+// on constant operands, which take less power; both are a million cycles, 840 to 855 a block.  What is left
+// over the MMAs: the warps of the epilogue that share a quarter of the SM with a warp of another role take
+// some 300 cycles a block longer, and the stores of a tile come on top (2000 cycles when its pieces went
+// out one at a time; two at a time, and the scales by two warps, took 2 % off the whole).
 //
 // Two tilings of one kernel:
 //   pair   : two CTAs (a cluster) compute a 256 x 256 tile with cta_group::2 MMAs, each of them 128
@@ -101,7 +104,8 @@ __device__ __forceinline__ uint4 pack16(const float* v, __nv_bfloat16) {
 
 // A warp's 32 rows x NC columns of Y, one row of sums a lane, through shared memory of its own in
 // pieces of 32 rows x 128 bytes: a lane's own row would go out as 16-byte pieces of 32 different lines
-// (measured 10,000 cycles for a 128 x 256 tile, the time of eleven blocks of the product; this way 2,000).
+// (measured 10,000 cycles for a 128 x 256 tile, the time of eleven blocks of the product; this way, a piece
+// at a time, 2,000).
 // Whole pieces leave by TMA stores, two at a time, which run on while the warp takes up the next tile; one
 // that an expert's last row cuts, or unaligned rows of Y, by stores of the lanes, 8 a row.  16-byte part p
 // of row r is kept at place p ^ (r % 8), the 128-byte swizzle of the tensor map.  Rows from `rows_left`
@@ -566,8 +570,9 @@ hq_status launch_fp8_gemm(const Fp8Gemm& p, int impl, cudaStream_t s) {
   }
 }
 
-// Few rows are quantised by the CTAs that multiply them, each the blocks that it needs: one launch.
-// More are quantised once, by a kernel of their own.
+// One to four rows are quantised by the CTAs that multiply them, each the blocks that it needs, where those
+// fit into its shared memory (few_quantises): one launch.  Others are quantised once, by a kernel of their
+// own.
 hq_status launch_fp8_linear(Fp8Gemm p, uint8_t* codes, float* scales, cudaStream_t s) {
   if (p.rows == 0) return HQ_OK;
   const int impl = pick_impl(p);

@@ -10,15 +10,19 @@
 // up the parts of some of the tile's rows of A, in the order of the CTAs, and stores them: no workspace,
 // no second launch, the same result every time.
 //
-// Of hq_fp8_linear's activations, one or a few rows are quantised here: the warps of a CTA turn the
-// blocks of its part of K into codes in shared memory while the first weights are on their way.  Every
-// tile's CTAs repeat that, but it reads little and saves a launch, which costs the host as long as the
-// kernel takes.  More rows are quantised by a kernel of their own and this one launched as its
+// Of hq_fp8_linear's activations, one to four rows are quantised here, where a CTA's part of K is 16
+// blocks at most: the warps of a CTA turn the blocks of its part into codes in shared memory while the first
+// weights are on their way.  Every tile's CTAs repeat that, but it reads little and saves a launch, which
+// costs the host as long as the kernel takes.  Other rows (one of 17408 x 5120, whose 136 tiles leave two
+// CTAs to each, 20 blocks a CTA) are quantised by a kernel of their own and this one launched as its
 // dependent, with the first weights loaded meanwhile: for 16 rows of 5120 11.0 us against 13.2 us.
 //
-// On the device, weights from DRAM: 1 x 5120 x 5120 9 us (set-up 0.8 us, 3 us to the first weights, the
-// cluster's sums 1.2 us), 1 x 17408 x 5120 18.5 us (4.8 TB/s), 24 x 17408 x 5120 19 us (4.8 TB/s); experts,
-// 512 rows of 48 2560 x 5120, 87 us (7.2 TB/s, nearly all of it reads).
+// hq_fp8_linear on the device, weights rotated through 1.2 GB so that all come from DRAM: 1 x 5120 x 5120
+// 10.2 us, 1 x 17408 x 5120 and 1 x 5120 x 17408 19.3 us, 24 x 17408 x 5120 22 us; experts, 512 rows of
+// 2560 x 5120, 39 of 48 of which have rows, 85 us (511 MB of weights, 6.0 TB/s).  All of these are about
+// 6 us and the weights at 6.5 TB/s: the 6 us are the launch, the set-up (0.8 us before the first load), 3 us
+// to the first weights and, where K is split, 1.2 us of the cluster's sums.  Experts' tiles do not split K:
+// one token's 8 experts of 768 x 2048 take 11 us, of 2560 x 5120 23 us (4.6 TB/s).
 //
 // Per CTA: warp 0 loads, warp 1 issues the MMAs, warp 2 leaves the products of the scales in shared
 // memory, warps 4-7 (one TMEM lane quadrant each) scale and add: a thread holds one row of W, that is a
@@ -405,7 +409,8 @@ constexpr int kSlots = kSMs * kCtasPerSM;
 // the variant that takes most shared memory, so that all variants of a tile height split alike and their
 // sums are the same; the device is assumed to be like the first one asked.  The runtime counts one CTA an
 // SM for kernels that allocate tensor memory; two of these run there (240 CTAs in clusters of 6 were seen
-// at once, 272 of 2), so its count is taken up by that.  0: not known.
+// at once, 272 of 2), so its count is taken up by that.  Where two did not run, clusters would wait for one
+// another: slower, with the same result.  0: not known.
 template <int BT>
 int clusters_at_once(int split) {
   using TX = typename std::conditional<BT == 16, __nv_bfloat16, uint8_t>::type;
