@@ -349,9 +349,10 @@ hq_status hq_fp8_quantize_blocks(const void* W, int w_dtype, int64_t E, int64_t 
  * hq_fp8_gemm: one weight for all M rows.  M >= 0 (M == 0 is a no-op).
  * hq_fp8_linear: the same from activations X [M, K] in x_dtype, quantised on the way (into the
  *   workspace, or, for up to four rows, by the product's own kernel): the result of
- *   hq_fp8_quantize_rows followed by hq_fp8_gemm, bit for bit.  workspace: device, 256-byte aligned, at least hq_fp8_linear_workspace_bytes(M, K) bytes (HQ_ERR_WORKSPACE), not
- *   shared with a call that may run at the same time (another stream, or another captured graph);
- *   NULL is accepted where that size is 0.
+ *   hq_fp8_quantize_rows followed by hq_fp8_gemm, bit for bit.  workspace: device, 256-byte aligned,
+ *   at least hq_fp8_linear_workspace_bytes(M, K) bytes (HQ_ERR_WORKSPACE), not shared with a call that
+ *   may run at the same time (another stream, or another captured graph); NULL is accepted where that
+ *   size is 0.
  * hq_fp8_expert_gemm: rows offsets[e] .. offsets[e + 1] - 1 of A and Y meet weight e of W
  *   [E, N, K], for every expert.  offsets: DEVICE int32 [E + 1], not decreasing, between 0 and
  *   `rows` (a range outside is cut to it, an inverted one is empty, and rows that ranges share hold

@@ -43,12 +43,12 @@ inline size_t round_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 // writes nothing and reads only what was written before its predecessor started (where that one was
 // launched the ordinary way: by anything before it on the stream).  What the predecessor writes is never
 // read by __ldg (ld.global.nc), which is for data that nothing writes while the kernel runs.
-// Along the factorisation's chain of short kernels (the small fp64 products, their split-K reduce, the
-// leaves) every kernel is chained to the next: it calls pdl_wait before touching memory, and
-// pdl_launch_dependents near its end, so that its successor is scheduled in turn without holding SM
-// slots for long (slots the second stream's work would otherwise use).  The e4m3 product behind its
-// quantiser, and the second half of the experts' sort, are the only links of theirs: the first kernel
-// lets the second start at once.  In a kernel launched the ordinary way both are no-ops.
+// The factorisation's short kernels (the small fp64 products, their split-K reduce, the leaves) follow one
+// another so: each calls pdl_wait before touching memory, and pdl_launch_dependents near its end, so that
+// its own successor is scheduled in turn without holding SM slots for long (slots the second stream's
+// work would otherwise use).  Of the e4m3 product behind its quantiser, and of the two kernels of the
+// experts' sort, the first lets the second start at once.  In a kernel launched the ordinary way both are
+// no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
